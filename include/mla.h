@@ -85,7 +85,8 @@ typedef struct {
 enum {
     MLA_STATUS_BAD_POS = 1,     /* append: pos[b] < 0 or pos[b] + n_tok > T_max */
     MLA_STATUS_BAD_SEQLEN = 2,  /* decode: seqlens[b] < q_len or > T_max */
-    MLA_STATUS_TIMEOUT = 4      /* a bounded device-side wait expired */
+    MLA_STATUS_TIMEOUT = 4,     /* a bounded device-side wait expired */
+    MLA_STATUS_NONFINITE = 8    /* packed append: a latent was NaN, infinite or larger than 13440 */
 };
 
 /* ---------------------------------------------------------------- a1: append
@@ -273,6 +274,115 @@ size_t mla_output_projection_workspace_bytes(const mla_dims_t* dims, int32_t row
 int mla_output_projection(const mla_dims_t* dims, const void* attn_out, const void* W_O, int32_t rows,
                           int32_t d_model, void* y, void* workspace, size_t workspace_bytes,
                           mla_stream_t stream);
+
+/* ---------------------------------------------------------------- 4-bit cache
+ * The latents of a token in 4 bits each with one 8-bit scale for every 16 of
+ * them, and the rotated RoPE key unquantised: 416 bytes a token in bf16 V3
+ * geometry instead of 1152, so 2.8 times the history in the same memory.
+ * A packed cache is an mla_cache_t whose elements are BYTES: strides in
+ * bytes, multiples of 16, stride_t >= mla_packed_row_bytes(); d_c must be a
+ * multiple of 16.  A row is
+ *   bytes [0, d_c/2)               codes n = q + 8, q in -7..7: in 32-bit word w, element 8w+2j
+ *                                  in bits 4j..4j+3, element 8w+2j+1 in bits 16+4j..19+4j
+ *   bytes [d_c/2, d_c/2 + d_c/16)  scales, byte e*8+m standing for 2^(e-21) (1 + m/8)
+ *   from there, rounded up to 16   the RoPE key in the call's dtype
+ * and stands for the latents q * scale, which are exact in bf16.  Rows that
+ * hold no token may hold any bytes. */
+size_t mla_packed_row_bytes(const mla_dims_t* dims);
+
+/* mla_append_cache for a packed cache: the latents of a group of 16 are
+ * rounded to the nearest of -7..7 times its scale (half to even), the
+ * smallest scale that is not below max|x| / 7.
+ *   pos   [B] int32   position of the first new token (its RoPE angle)
+ *   rows  [B] int32   row it is written to; NULL: pos.  They differ once
+ *                     rows have been evicted.
+ * A sequence whose rows or positions are out of range is skipped and flags
+ * MLA_STATUS_BAD_POS.  A NaN latent is stored as 0 and one above 13440 (the
+ * largest scale times 7) as 13440; both flag MLA_STATUS_NONFINITE. */
+int mla_append_packed(const mla_dims_t* dims, const void* c_kv, const void* k_rope, const int32_t* pos,
+                      const int32_t* rows, int32_t B, int32_t n_tok, const mla_cache_t* cache, mla_stream_t stream);
+
+/* mla_append_cache with the row apart from the position, for a full-width
+ * cache from which rows have been evicted (arguments as above). */
+int mla_append_rows(const mla_dims_t* dims, const void* c_kv, const void* k_rope, const int32_t* pos,
+                    const int32_t* rows, int32_t B, int32_t n_tok, const mla_cache_t* cache, mla_stream_t stream);
+
+/* Rows rows[b] .. rows[b] + n_tok - 1 of a packed cache as full-width rows,
+ * out [B][n_tok][d_c + d_r]: what a full-width cache of the same tokens
+ * would hold after quantisation.  Rows out of range are written as zeros and flag
+ * MLA_STATUS_BAD_POS. */
+int mla_load_packed(const mla_dims_t* dims, const mla_cache_t* cache, const int32_t* rows, int32_t B, int32_t n_tok,
+                    void* out, mla_stream_t stream);
+
+/* Bytes of scratch mla_decode_packed / mla_attend_packed need. */
+size_t mla_packed_workspace_bytes(const mla_dims_t* dims, int32_t B, int32_t q_len);
+
+/* mla_attend_latent over a packed cache.  lse [B][q_len][H] fp32 (may be
+ * NULL) receives the natural log of the sum over keys of exp(s_j), -infinity
+ * for a sequence with an invalid length.  Of the options, path, num_pairs,
+ * overhead_tiles, min_tiles (both in 128-key tiles here) and wait_limit_ns
+ * apply. */
+int mla_attend_packed(const mla_dims_t* dims, const void* q_hat, const mla_cache_t* cache, const int32_t* seqlens,
+                      int32_t B, int32_t q_len, void* o_lat, float* lse, void* workspace, size_t workspace_bytes,
+                      const mla_decode_opts_t* opts, mla_stream_t stream);
+
+/* mla_decode over a packed cache.  seqlens[b] counts the rows of the cache,
+ * n_seen[b] the tokens the sequence has had (both including the q_len new
+ * ones): query i sits at position n_seen[b] - q_len + i.  n_seen may be NULL
+ * where no row has been evicted (then it is seqlens).  q_hat
+ * [B][q_len][H][d_c + d_r] and lse [B][q_len][H] receive the folded queries
+ * and the log-sum-exps, for mla_accumulate_weights; either may be NULL. */
+int mla_decode_packed(const mla_dims_t* dims, const void* q_nope, const void* q_rope, const void* W_UK,
+                      const void* W_UV, const mla_cache_t* cache, const int32_t* seqlens, const int32_t* n_seen,
+                      int32_t B, int32_t q_len, void* out, void* q_hat, float* lse, void* workspace,
+                      size_t workspace_bytes, const mla_decode_opts_t* opts, mla_stream_t stream);
+
+/* ---------------------------------------------------------------- eviction by accumulated attention weight
+ * A cache kept within a budget of rows: after each step every row's
+ * attention weight is added to a running sum, and when a sequence outgrows
+ * the budget the rows with the least are dropped.  Rows keep their rotated keys, so
+ * after an eviction a sequence's row count and its token count differ:
+ * append with mla_append_rows / mla_append_packed, fold the queries with the
+ * token counts (mla_absorb_query's seqlens, mla_decode_packed's n_seen) and
+ * attend with the row counts. */
+enum { MLA_CACHE_FULL = 0, MLA_CACHE_PACKED = 1 }; /* cache_format */
+
+/* mla_attend_latent that also writes the log-sum-exps, as mla_attend_packed does (lse not NULL). */
+int mla_attend_latent_lse(const mla_dims_t* dims, const void* q_hat, const mla_cache_t* cache, const int32_t* seqlens,
+                          int32_t B, int32_t q_len, void* o_lat, float* lse, void* workspace, size_t workspace_bytes,
+                          const mla_decode_opts_t* opts, mla_stream_t stream);
+
+/* weights[b][t] = decay * prev[b][t] + sum_{i,h} exp(softmax_scale * q_hat[b][i][h] . row_t - lse[b][i][h])
+ * for the rows t < seqlens[b] (query i counts where it sees the row; a row of lse that is -infinity counts nothing).
+ *   lse     [B][q_len][H] fp32   of the same step over the same cache
+ *   prev    [B][weights_stride] fp32, may be weights itself, or NULL (zero)
+ *   weights [B][weights_stride] fp32; entries of rows >= seqlens[b], and of a
+ *           sequence with an invalid length (flags MLA_STATUS_BAD_SEQLEN), are left as they were
+ * weights_stride >= T_max.  The sums do not depend on how the work is spread (no atomics).
+ * Of the options, path and wait_limit_ns apply. */
+int mla_accumulate_weights(const mla_dims_t* dims, const void* q_hat, const float* lse, const mla_cache_t* cache,
+                           int32_t cache_format, const int32_t* seqlens, int32_t B, int32_t q_len, float decay,
+                           const float* prev, float* weights, int64_t weights_stride, const mla_decode_opts_t* opts,
+                           mla_stream_t stream);
+
+/* Cuts every sequence of more than `budget` rows down to budget rows: its
+ * first n_sink, its last n_recent, and of the rows between the
+ * budget - n_sink - n_recent with the largest weights (equal weights: the
+ * lower row; a NaN counts as less than any number).  The kept rows, in their
+ * order, become rows 0.. of out_cache, their weights out_weights[b][0..], and
+ * out_seqlens[b] their number; shorter sequences are kept whole.
+ *   kept  [B][budget] int32, may be NULL: the kept rows' indexes, -1 past their number
+ * out_cache may be the cache itself, out_weights weights, out_seqlens seqlens
+ * (eviction in place); other overlaps are refused.  Rows of out_cache and entries of
+ * out_weights past the kept ones are left as they were.  A sequence with a
+ * negative length or one above T_max keeps nothing and flags
+ * MLA_STATUS_BAD_SEQLEN.  The workspace is of mla_evict_workspace_bytes()
+ * bytes, 16-byte aligned, the call's until the stream reaches its end. */
+size_t mla_evict_workspace_bytes(const mla_dims_t* dims, int32_t cache_format, int32_t B, int32_t budget);
+int mla_evict(const mla_dims_t* dims, const mla_cache_t* cache, int32_t cache_format, const float* weights,
+              int64_t weights_stride, const int32_t* seqlens, int32_t B, int32_t budget, int32_t n_sink,
+              int32_t n_recent, const mla_cache_t* out_cache, float* out_weights, int64_t out_weights_stride,
+              int32_t* out_seqlens, int32_t* kept, void* workspace, size_t workspace_bytes, mla_stream_t stream);
 
 /* ---------------------------------------------------------------- status */
 

@@ -20,7 +20,8 @@ LIB_PATH = os.path.join(_HERE, "libmla.so")
 
 MLA_DTYPE_BF16, MLA_DTYPE_F32 = 0, 1
 PATH_AUTO, PATH_SM100, PATH_GENERIC = 0, 1, 2
-STATUS_BAD_POS, STATUS_BAD_SEQLEN, STATUS_TIMEOUT = 1, 2, 4
+STATUS_BAD_POS, STATUS_BAD_SEQLEN, STATUS_TIMEOUT, STATUS_NONFINITE = 1, 2, 4, 8
+CACHE_FULL, CACHE_PACKED = 0, 1
 NUM_EVENTS = 6
 EV_START, EV_ABSORB_DONE, EV_ATTEND_BEGIN, EV_ATTEND_END, EV_COMBINE_DONE, EV_END = range(6)
 ERRORS = {-1: "MLA_ERR_ARG", -2: "MLA_ERR_SHAPE", -3: "MLA_ERR_ALIGN", -4: "MLA_ERR_CUDA",
@@ -30,7 +31,9 @@ ERRORS = {-1: "MLA_ERR_ARG", -2: "MLA_ERR_SHAPE", -3: "MLA_ERR_ALIGN", -4: "MLA_
 EXPORTS = ["mla_append_cache", "mla_workspace_bytes", "mla_decode", "mla_decode_ex", "mla_absorb_query",
            "mla_attend_latent", "mla_project_out", "mla_device_status", "mla_last_error", "mla_last_path",
            "mla_version", "mla_decode_no_alloc", "mla_append_from_hidden", "mla_append_from_hidden_workspace_bytes",
-           "mla_output_projection", "mla_output_projection_workspace_bytes"]
+           "mla_output_projection", "mla_output_projection_workspace_bytes", "mla_packed_row_bytes", "mla_append_packed",
+           "mla_append_rows", "mla_load_packed", "mla_packed_workspace_bytes", "mla_attend_packed", "mla_decode_packed",
+           "mla_attend_latent_lse", "mla_accumulate_weights", "mla_evict_workspace_bytes", "mla_evict"]
 
 
 class Dims(ctypes.Structure):
@@ -77,6 +80,22 @@ _SIGS = {
                                 ctypes.c_size_t, _P], ctypes.c_int),
     "mla_output_projection_workspace_bytes": ([ctypes.POINTER(Dims), _I, _I], ctypes.c_size_t),
     "mla_output_projection": ([ctypes.POINTER(Dims), _P, _P, _I, _I, _P, _P, ctypes.c_size_t, _P], ctypes.c_int),
+    "mla_packed_row_bytes": ([ctypes.POINTER(Dims)], ctypes.c_size_t),
+    "mla_append_packed": ([ctypes.POINTER(Dims), _P, _P, _P, _P, _I, _I, ctypes.POINTER(Cache), _P], ctypes.c_int),
+    "mla_append_rows": ([ctypes.POINTER(Dims), _P, _P, _P, _P, _I, _I, ctypes.POINTER(Cache), _P], ctypes.c_int),
+    "mla_load_packed": ([ctypes.POINTER(Dims), ctypes.POINTER(Cache), _P, _I, _I, _P, _P], ctypes.c_int),
+    "mla_packed_workspace_bytes": ([ctypes.POINTER(Dims), _I, _I], ctypes.c_size_t),
+    "mla_attend_packed": ([ctypes.POINTER(Dims), _P, ctypes.POINTER(Cache), _P, _I, _I, _P, _P, _P, ctypes.c_size_t,
+                           ctypes.POINTER(Opts), _P], ctypes.c_int),
+    "mla_decode_packed": ([ctypes.POINTER(Dims), _P, _P, _P, _P, ctypes.POINTER(Cache), _P, _P, _I, _I, _P, _P, _P, _P,
+                           ctypes.c_size_t, ctypes.POINTER(Opts), _P], ctypes.c_int),
+    "mla_attend_latent_lse": ([ctypes.POINTER(Dims), _P, ctypes.POINTER(Cache), _P, _I, _I, _P, _P, _P, ctypes.c_size_t,
+                               ctypes.POINTER(Opts), _P], ctypes.c_int),
+    "mla_accumulate_weights": ([ctypes.POINTER(Dims), _P, _P, ctypes.POINTER(Cache), _I, _P, _I, _I, ctypes.c_float, _P,
+                                _P, ctypes.c_int64, ctypes.POINTER(Opts), _P], ctypes.c_int),
+    "mla_evict_workspace_bytes": ([ctypes.POINTER(Dims), _I, _I, _I], ctypes.c_size_t),
+    "mla_evict": ([ctypes.POINTER(Dims), ctypes.POINTER(Cache), _I, _P, ctypes.c_int64, _P, _I, _I, _I, _I,
+                   ctypes.POINTER(Cache), _P, ctypes.c_int64, _P, _P, _P, ctypes.c_size_t, _P], ctypes.c_int),
     "mla_device_status": ([_P, ctypes.POINTER(_I)], ctypes.c_int),
     "mla_last_error": ([], ctypes.c_char_p),
     "mla_last_path": ([], ctypes.c_char_p),
@@ -111,6 +130,26 @@ def _need(t: torch.Tensor, name: str, dtype=None, ndim=None):
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if ndim is not None and t.dim() != ndim:
         raise ValueError(f"{name} must have {ndim} dims, got {tuple(t.shape)}")
+
+
+def _need_all(device, **tensors):
+    """Each (tensor, dtype, shape) is a contiguous CUDA tensor of that type and shape on ``device``; None passes."""
+    for name, (t, dtype, shape) in tensors.items():
+        if t is None:
+            continue
+        _need(t, name, dtype=dtype)
+        if tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+        if t.device != device:
+            raise ValueError(f"{name} is on {t.device}, the other tensors on {device}")
+
+
+def _need_weights(t, name, device, B):
+    """Running weights: fp32 [B][>= T_max], unit stride along the rows (a view of a larger array is passed on)."""
+    if t.dtype != torch.float32 or t.dim() != 2 or t.shape[0] != B or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be fp32 [{B}, rows] with unit stride along the rows")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the other tensors on {device}")
 
 
 class Library:
@@ -280,6 +319,204 @@ class Library:
         self._check(self.lib.mla_output_projection(ctypes.byref(dims), _ptr(attn_out), _ptr(W_O), rows, d_model,
                                                    _ptr(y), _ptr(workspace), workspace.numel(), _stream(stream)))
         return y
+
+    # ------------------------------------------------------------------ 4-bit cache
+    @staticmethod
+    def _dtype(dims: Dims) -> torch.dtype:
+        return torch.float32 if dims.dtype == MLA_DTYPE_F32 else torch.bfloat16
+
+    def packed_row_bytes(self, dims: Dims) -> int:
+        """Bytes of a packed row; a packed cache is a uint8 tensor [B][T_max][row bytes]."""
+        n = int(self.lib.mla_packed_row_bytes(ctypes.byref(dims)))
+        if n == 0:
+            raise ValueError("these dims have no packed row (d_c must be a multiple of 16)")
+        return n
+
+    def _any_cache(self, dims: Dims, cache: torch.Tensor, name: str = "cache", device=None):
+        """(descriptor, format) of a full-width or (uint8) packed cache."""
+        packed = cache.dtype == torch.uint8
+        if not packed and cache.dtype != self._dtype(dims):
+            raise TypeError(f"{name} must be {self._dtype(dims)} or torch.uint8 (packed), got {cache.dtype}")
+        d = self.cache_desc(cache)
+        row = self.packed_row_bytes(dims) if packed else dims.d_c + dims.d_r
+        if cache.shape[2] < row:
+            raise ValueError(f"{name} rows hold {cache.shape[2]} elements, {row} are needed")
+        if device is not None and cache.device != device:
+            raise ValueError(f"{name} is on {cache.device}, the other tensors on {device}")
+        return d, CACHE_PACKED if packed else CACHE_FULL
+
+    def _packed_cache(self, dims: Dims, cache: torch.Tensor, device) -> Cache:
+        d, fmt = self._any_cache(dims, cache, device=device)
+        if fmt != CACHE_PACKED:
+            raise TypeError(f"a packed cache is torch.uint8, got {cache.dtype}")
+        return d
+
+    def _append(self, fn, dims, cd, c_kv, k_rope, pos, rows, stream):
+        dt = self._dtype(dims)
+        _need(c_kv, "c_kv", dtype=dt, ndim=3)
+        B, n_tok = c_kv.shape[0], c_kv.shape[1]
+        _need_all(c_kv.device, c_kv=(c_kv, dt, (B, n_tok, dims.d_c)), k_rope=(k_rope, dt, (B, n_tok, dims.d_r)),
+                  pos=(pos, torch.int32, (B,)), rows=(rows, torch.int32, (B,)))
+        with torch.cuda.device(c_kv.device):
+            self._check(fn(ctypes.byref(dims), _ptr(c_kv), _ptr(k_rope), _ptr(pos), _ptr(rows), B, n_tok,
+                           ctypes.byref(cd), _stream(stream)))
+
+    def append_packed(self, dims: Dims, cache: torch.Tensor, c_kv: torch.Tensor, k_rope: torch.Tensor,
+                      pos: torch.Tensor, rows: Optional[torch.Tensor] = None, stream=None):
+        """Rows rows[b]+i (default pos[b]+i) of the packed cache <- [c_kv[b,i] in 4 bits || RoPE(k_rope[b,i], pos[b]+i)]."""
+        cd = self._packed_cache(dims, cache, c_kv.device)
+        self._append(self.lib.mla_append_packed, dims, cd, c_kv, k_rope, pos, rows, stream)
+
+    def append_rows(self, dims: Dims, cache: torch.Tensor, c_kv: torch.Tensor, k_rope: torch.Tensor, pos: torch.Tensor,
+                    rows: torch.Tensor, stream=None):
+        """append_cache with the row apart from the position (after rows have been evicted)."""
+        cd, fmt = self._any_cache(dims, cache, device=c_kv.device)
+        if fmt != CACHE_FULL:
+            raise TypeError("append_rows writes full-width rows: use append_packed for a packed cache")
+        self._append(self.lib.mla_append_rows, dims, cd, c_kv, k_rope, pos, rows, stream)
+
+    def load_packed(self, dims: Dims, cache: torch.Tensor, rows: torch.Tensor, n_tok: int, out=None, stream=None):
+        """Rows rows[b] .. rows[b]+n_tok-1 as full-width rows [B, n_tok, d_c + d_r]."""
+        _need(rows, "rows", dtype=torch.int32, ndim=1)
+        cd = self._packed_cache(dims, cache, rows.device)
+        shape = (rows.shape[0], n_tok, dims.d_c + dims.d_r)
+        if out is None:
+            out = torch.empty(shape, dtype=self._dtype(dims), device=rows.device)
+        _need_all(rows.device, out=(out, self._dtype(dims), shape))
+        with torch.cuda.device(rows.device):
+            self._check(self.lib.mla_load_packed(ctypes.byref(dims), ctypes.byref(cd), _ptr(rows), shape[0], n_tok,
+                                                 _ptr(out), _stream(stream)))
+        return out
+
+    def packed_workspace_bytes(self, dims: Dims, B: int, q_len: int) -> int:
+        return int(self.lib.mla_packed_workspace_bytes(ctypes.byref(dims), B, q_len))
+
+    def _workspace(self, workspace, nbytes, device):
+        if workspace is None:
+            return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
+        _need(workspace, "workspace", dtype=torch.uint8)
+        if workspace.device != device:
+            raise ValueError(f"workspace is on {workspace.device}, the other tensors on {device}")
+        return workspace
+
+    def attend_packed(self, dims: Dims, q_hat, cache, seqlens, out=None, lse=None, workspace=None,
+                      opts: Optional[Opts] = None, stream=None):
+        """attend_latent over a packed cache; ``lse`` (fp32 [B, q_len, H]) receives the log-sum-exps if given."""
+        dt, dev = self._dtype(dims), q_hat.device
+        _need(q_hat, "q_hat", dtype=dt, ndim=4)
+        B, q_len = q_hat.shape[0], q_hat.shape[1]
+        cd = self._packed_cache(dims, cache, dev)
+        if out is None:
+            out = torch.empty((B, q_len, dims.H, dims.d_c), dtype=dt, device=dev)
+        _need_all(dev, q_hat=(q_hat, dt, (B, q_len, dims.H, dims.d_c + dims.d_r)), seqlens=(seqlens, torch.int32, (B,)),
+                  out=(out, dt, (B, q_len, dims.H, dims.d_c)), lse=(lse, torch.float32, (B, q_len, dims.H)))
+        with torch.cuda.device(dev):
+            ws = self._workspace(workspace, 0 if workspace is not None else self.packed_workspace_bytes(dims, B, q_len), dev)
+            self._check(self.lib.mla_attend_packed(ctypes.byref(dims), _ptr(q_hat), ctypes.byref(cd), _ptr(seqlens), B,
+                                                   q_len, _ptr(out), _ptr(lse), _ptr(ws), ws.numel(),
+                                                   ctypes.byref(opts) if opts is not None else None, _stream(stream)))
+        return out
+
+    def decode_packed(self, dims: Dims, q_nope, q_rope, W_UK, W_UV, cache, seqlens, n_seen=None, out=None, q_hat=None,
+                      lse=None, workspace=None, opts: Optional[Opts] = None, stream=None):
+        """One decode step over a packed cache; returns out [B, q_len, H, d_v].  ``seqlens`` counts rows, ``n_seen``
+        tokens (default: the same); ``q_hat`` and ``lse`` receive the folded queries and log-sum-exps if given."""
+        dt, dev = self._dtype(dims), q_nope.device
+        _need(q_nope, "q_nope", dtype=dt, ndim=4)
+        B, q_len = q_nope.shape[0], q_nope.shape[1]
+        cd = self._packed_cache(dims, cache, dev)
+        if out is None:
+            out = torch.empty((B, q_len, dims.H, dims.d_v), dtype=dt, device=dev)
+        _need_all(dev, q_nope=(q_nope, dt, (B, q_len, dims.H, dims.d_n)), q_rope=(q_rope, dt, (B, q_len, dims.H, dims.d_r)),
+                  W_UK=(W_UK, dt, (dims.H, dims.d_n, dims.d_c)), W_UV=(W_UV, dt, (dims.H, dims.d_v, dims.d_c)),
+                  seqlens=(seqlens, torch.int32, (B,)), n_seen=(n_seen, torch.int32, (B,)),
+                  out=(out, dt, (B, q_len, dims.H, dims.d_v)), q_hat=(q_hat, dt, (B, q_len, dims.H, dims.d_c + dims.d_r)),
+                  lse=(lse, torch.float32, (B, q_len, dims.H)))
+        with torch.cuda.device(dev):
+            ws = self._workspace(workspace, 0 if workspace is not None else self.packed_workspace_bytes(dims, B, q_len), dev)
+            self._check(self.lib.mla_decode_packed(ctypes.byref(dims), _ptr(q_nope), _ptr(q_rope), _ptr(W_UK), _ptr(W_UV),
+                                                   ctypes.byref(cd), _ptr(seqlens), _ptr(n_seen), B, q_len, _ptr(out),
+                                                   _ptr(q_hat), _ptr(lse), _ptr(ws), ws.numel(),
+                                                   ctypes.byref(opts) if opts is not None else None, _stream(stream)))
+        return out
+
+    # ------------------------------------------------------------------ eviction by accumulated attention weight
+    def attend_latent_lse(self, dims: Dims, q_hat, cache, seqlens, lse, out=None, workspace=None,
+                          opts: Optional[Opts] = None, stream=None):
+        """attend_latent that also writes the log-sum-exps to ``lse`` (fp32 [B, q_len, H])."""
+        dt, dev = self._dtype(dims), q_hat.device
+        _need(q_hat, "q_hat", dtype=dt, ndim=4)
+        B, q_len = q_hat.shape[0], q_hat.shape[1]
+        cd, fmt = self._any_cache(dims, cache, device=dev)
+        if fmt != CACHE_FULL:
+            raise TypeError("attend_latent_lse reads full-width rows: use attend_packed for a packed cache")
+        if out is None:
+            out = torch.empty((B, q_len, dims.H, dims.d_c), dtype=dt, device=dev)
+        _need_all(dev, q_hat=(q_hat, dt, (B, q_len, dims.H, dims.d_c + dims.d_r)), seqlens=(seqlens, torch.int32, (B,)),
+                  out=(out, dt, (B, q_len, dims.H, dims.d_c)), lse=(lse, torch.float32, (B, q_len, dims.H)))
+        with torch.cuda.device(dev):
+            ws = self._workspace(workspace, 0 if workspace is not None else self.workspace_bytes(dims, B, q_len), dev)
+            self._check(self.lib.mla_attend_latent_lse(ctypes.byref(dims), _ptr(q_hat), ctypes.byref(cd), _ptr(seqlens), B,
+                                                       q_len, _ptr(out), _ptr(lse), _ptr(ws), ws.numel(),
+                                                       ctypes.byref(opts) if opts is not None else None, _stream(stream)))
+        return out
+
+    def accumulate_weights(self, dims: Dims, q_hat, lse, cache, seqlens, weights, prev=None, decay: float = 1.0,
+                           opts: Optional[Opts] = None, stream=None):
+        """weights[b, t] = decay * prev[b, t] + the attention weight row t received in this step, summed over heads and
+        queries (``prev``: None for zero, or ``weights`` itself); the cache is full-width or packed."""
+        dt, dev = self._dtype(dims), q_hat.device
+        _need(q_hat, "q_hat", dtype=dt, ndim=4)
+        B, q_len = q_hat.shape[0], q_hat.shape[1]
+        cd, fmt = self._any_cache(dims, cache, device=dev)
+        _need_all(dev, q_hat=(q_hat, dt, (B, q_len, dims.H, dims.d_c + dims.d_r)), lse=(lse, torch.float32, (B, q_len, dims.H)),
+                  seqlens=(seqlens, torch.int32, (B,)))
+        _need_weights(weights, "weights", dev, B)
+        if weights.shape[1] < cache.shape[1]:
+            raise ValueError(f"weights cover {weights.shape[1]} rows, the cache holds {cache.shape[1]}")
+        stride = weights.stride(0) if B > 1 else max(weights.stride(0), cache.shape[1])
+        if prev is not None:
+            _need_weights(prev, "prev", dev, B)
+            if prev.shape != weights.shape or (B > 1 and prev.stride(0) != weights.stride(0)):
+                raise ValueError("prev must have the shape and strides of weights")
+        with torch.cuda.device(dev):
+            self._check(self.lib.mla_accumulate_weights(ctypes.byref(dims), _ptr(q_hat), _ptr(lse), ctypes.byref(cd), fmt,
+                                                        _ptr(seqlens), B, q_len, decay, _ptr(prev), _ptr(weights), stride,
+                                                        ctypes.byref(opts) if opts is not None else None, _stream(stream)))
+        return weights
+
+    def evict_workspace_bytes(self, dims: Dims, B: int, budget: int, packed: bool = False) -> int:
+        fmt = CACHE_PACKED if packed else CACHE_FULL
+        return int(self.lib.mla_evict_workspace_bytes(ctypes.byref(dims), fmt, B, budget))
+
+    def evict(self, dims: Dims, cache, weights, seqlens, budget: int, n_sink: int = 0, n_recent: int = 0, out=None,
+              out_weights=None, out_seqlens=None, kept=None, workspace=None, stream=None):
+        """Cuts sequences of more than ``budget`` rows down to the first n_sink, the last n_recent and the rows between
+        with the largest weights, in their order.  In place unless ``out`` / ``out_weights`` / ``out_seqlens`` are
+        given; ``kept`` (int32 [B, budget]) receives the kept rows' indexes, -1 past their number."""
+        _need(seqlens, "seqlens", dtype=torch.int32, ndim=1)
+        dev, B = seqlens.device, seqlens.shape[0]
+        out = cache if out is None else out
+        out_weights = weights if out_weights is None else out_weights
+        out_seqlens = seqlens if out_seqlens is None else out_seqlens
+        cd, fmt = self._any_cache(dims, cache, device=dev)
+        od, out_fmt = self._any_cache(dims, out, "out", device=dev)
+        if fmt != out_fmt:
+            raise TypeError("out must be of the cache's kind")
+        _need_weights(weights, "weights", dev, B)
+        _need_weights(out_weights, "out_weights", dev, B)
+        most = min(budget, cache.shape[1])
+        if weights.shape[1] < cache.shape[1] or out_weights.shape[1] < most:
+            raise ValueError(f"weights must cover {cache.shape[1]} rows and out_weights {most}")
+        _need_all(dev, out_seqlens=(out_seqlens, torch.int32, (B,)), kept=(kept, torch.int32, (B, budget)))
+        sw = weights.stride(0) if B > 1 else max(weights.stride(0), cache.shape[1])
+        so = sw if out_weights is weights else (out_weights.stride(0) if B > 1 else max(out_weights.stride(0), most))
+        with torch.cuda.device(dev):
+            n = 0 if workspace is not None else self.evict_workspace_bytes(dims, B, budget, fmt == CACHE_PACKED)
+            ws = self._workspace(workspace, n, dev)
+            self._check(self.lib.mla_evict(ctypes.byref(dims), ctypes.byref(cd), fmt, _ptr(weights), sw, _ptr(seqlens), B,
+                                           budget, n_sink, n_recent, ctypes.byref(od), _ptr(out_weights), so,
+                                           _ptr(out_seqlens), _ptr(kept), _ptr(ws), ws.numel(), _stream(stream)))
 
     def device_status(self, stream=None) -> int:
         """Synchronises the stream, returns and clears the device status bits."""

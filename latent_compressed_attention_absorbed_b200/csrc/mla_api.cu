@@ -43,8 +43,25 @@ int current_device() {
     return d;
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+struct DecodeLayout {
+    size_t q_hat, o_lat, attend, total;
+};
+
+DecodeLayout decode_layout(const Problem& p, bool fast, int pairs) {
+    Carve c(nullptr);
+    DecodeLayout L;
+    const size_t U = (size_t)p.B * p.q_len * p.H;
+    L.q_hat = c.off;
+    c.take(U * (p.d_c + p.d_r) * elem_size(p));
+    L.o_lat = c.off;
+    c.take(U * p.d_c * elem_size(p));
+    L.attend = c.off;
+    if (fast) c.take(sm100_attend_workspace_bytes(p, pairs));
+    L.total = c.off;
+    return L;
+}
+
+}  // namespace
 
 int check_dims(const mla_dims_t* d, Problem* p) {
     if (!d) return fail(MLA_ERR_ARG, "dims is NULL");
@@ -71,8 +88,6 @@ int check_dims(const mla_dims_t* d, Problem* p) {
         p->rope.inv_freq[k] = (k < d->d_r / 2) ? pow((double)d->rope_base, -2.0 * k / (double)d->d_r) : 0.0;
     return MLA_OK;
 }
-
-size_t elem_size(const Problem& p) { return p.dtype == MLA_DTYPE_F32 ? 4 : 2; }
 
 int check_cache(const Problem& p, const mla_cache_t* c, int B, CacheView* v) {
     if (!c || !c->data) return fail(MLA_ERR_ARG, "cache or cache->data is NULL");
@@ -119,33 +134,12 @@ int pairs_for(const mla_decode_opts_t* o) {
 // The kernels store 32-byte vectors into the workspace; its base is rounded up
 // to 256 bytes inside the caller's buffer (mla_workspace_bytes includes the
 // slack), so any 16-byte-aligned buffer of that size works.
-constexpr size_t kWsAlign = 256;
 void* align_ws(void* ws, size_t* bytes) {
     const uintptr_t p = reinterpret_cast<uintptr_t>(ws);
     const uintptr_t a = (p + kWsAlign - 1) & ~uintptr_t(kWsAlign - 1);
     *bytes = (a - p) > *bytes ? 0 : *bytes - (a - p);
     return reinterpret_cast<void*>(a);
 }
-
-struct DecodeLayout {
-    size_t q_hat, o_lat, attend, total;
-};
-
-DecodeLayout decode_layout(const Problem& p, bool fast, int pairs) {
-    Carve c(nullptr);
-    DecodeLayout L;
-    const size_t U = (size_t)p.B * p.q_len * p.H;
-    L.q_hat = c.off;
-    c.take(U * (p.d_c + p.d_r) * elem_size(p));
-    L.o_lat = c.off;
-    c.take(U * p.d_c * elem_size(p));
-    L.attend = c.off;
-    if (fast) c.take(sm100_attend_workspace_bytes(p, pairs));
-    L.total = c.off;
-    return L;
-}
-
-}  // namespace
 
 int set_error(int code, const char* fmt, ...) {
     va_list ap;

@@ -51,6 +51,19 @@ struct Carve {
 // Records the thread's last-error text (read by mla_last_error) and returns `code`.
 int set_error(int code, const char* fmt, ...);
 
+// Argument checks and choices shared by the entry points (each records the
+// thread's error text and returns an MLA_ERR_* code on refusal).
+int check_dims(const mla_dims_t* d, Problem* p);
+int check_cache(const Problem& p, const mla_cache_t* c, int B, CacheView* v);
+// Which path serves the call; also what mla_last_path() then says.
+int choose_path(const Problem& p, int q_len, const mla_decode_opts_t* o, bool* fast);
+int pairs_for(const mla_decode_opts_t* o);
+constexpr size_t kWsAlign = 256;
+void* align_ws(void* ws, size_t* bytes);
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+inline size_t elem_size(const Problem& p) { return p.dtype == MLA_DTYPE_F32 ? 4 : 2; }
+
 // Device status word of the current device (set up once per device).
 int* device_status_ptr();
 
@@ -86,7 +99,7 @@ cudaError_t sm100_attend(const Problem& p, const void* q_hat, const CacheView& c
                          void* o_lat, void* workspace, size_t ws_bytes, int num_pairs, int overhead_tiles,
                          int min_tiles, int* status, cudaStream_t st, const Events* events = nullptr,
                          bool plan_ready = false, bool combine = true, const void* prefetch = nullptr,
-                         size_t prefetch_bytes = 0, const mla_decode_opts_t* opts = nullptr);
+                         size_t prefetch_bytes = 0, const mla_decode_opts_t* opts = nullptr, float* lse = nullptr);
 cudaError_t sm100_project(const Problem& p, const void* o_lat, const void* W_UV, int rows, void* out,
                           cudaStream_t st);
 // Small batches: matrix-vector kernels.  The project step (B * q_len <= 8)

@@ -280,7 +280,8 @@ size_t sm100_attend_workspace_bytes(const Problem& p, int num_pairs) {
 cudaError_t sm100_attend(const Problem& p, const void* q_hat, const CacheView& cache, const int32_t* seqlens,
                          void* o_lat, void* workspace, size_t ws_bytes, int num_pairs, int overhead_tiles,
                          int min_tiles, int* status, cudaStream_t st, const Events* events, bool plan_ready,
-                         bool combine, const void* prefetch, size_t prefetch_bytes, const mla_decode_opts_t* opts) {
+                         bool combine, const void* prefetch, size_t prefetch_bytes, const mla_decode_opts_t* opts,
+                         float* lse) {
     const int clusters = attend_clusters(num_pairs, p.q_len);
     if (clusters / p.q_len > kPlanMaxGroups) return cudaErrorInvalidValue;
     size_t off_part, off_lse;
@@ -299,7 +300,7 @@ cudaError_t sm100_attend(const Problem& p, const void* q_hat, const CacheView& c
     cudaError_t e;
     if (!plan_ready) {
         mla_plan_kernel<<<1, 32, 0, st>>>(seqlens, p.B, p.q_len, cache.T_max, clusters, plan_ovh(overhead_tiles),
-                                          plan_min_units(min_tiles), plan, status, (__nv_bfloat16*)o_lat);
+                                          plan_min_units(min_tiles), plan, status, (__nv_bfloat16*)o_lat, lse);
         e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
@@ -318,6 +319,7 @@ cudaError_t sm100_attend(const Problem& p, const void* q_hat, const CacheView& c
     a.prefetch_bytes = prefetch ? prefetch_bytes : 0;
     a.part_o = reinterpret_cast<float*>(ws + off_part);
     a.part_lse = reinterpret_cast<float*>(ws + off_lse);
+    a.lse = lse;
     a.status = status;
     a.wait_limit_ns = (opts && opts->wait_limit_ns > 0) ? (uint64_t)opts->wait_limit_ns : MLA_WAIT_LIMIT_NS;
     a.withhold_tile = (opts && opts->withhold_tile > 0) ? opts->withhold_tile : -1;
@@ -337,7 +339,7 @@ cudaError_t sm100_attend(const Problem& p, const void* q_hat, const CacheView& c
     const int max_split = units < clusters ? units : clusters;
     if (combine)
         e = launch_pdl(mla_combine_kernel, dim3(max_split * (kHeads / 8)), dim3(256), 0, st, 1, (const Plan*)plan,
-                       (const float*)a.part_o, (const float*)a.part_lse, (__nv_bfloat16*)o_lat);
+                       (const float*)a.part_o, (const float*)a.part_lse, (__nv_bfloat16*)o_lat, lse);
     if (e != cudaSuccess) return e;
     return cudaGetLastError();
 }

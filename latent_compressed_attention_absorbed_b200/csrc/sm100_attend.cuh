@@ -325,6 +325,7 @@ struct AttendArgs {
     size_t prefetch_bytes;        // (the next step's weights when this step's own traffic is small)
     float* part_o;                // [slots][64 column octets][128 heads][8]
     float* part_lse;              // [slots][128]
+    float* lse;                   // optional: natural-log LSE of every row, [B][q_len][128]
     int* status;
     uint64_t wait_limit_ns;       // time limit of every barrier wait
     int withhold_tile;            // test hook (>= 0): the loaders stop before this tile (see mla.h)
@@ -340,6 +341,11 @@ struct AttendArgs {
 __device__ __forceinline__ uint32_t sw128(int r, int c) { return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)); }
 // The same for 64-byte rows (SW64: chunk c of row r moves to c ^ ((r / 2) % 4)).
 __device__ __forceinline__ uint32_t sw64(int r, int c) { return (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3)) << 4)); }
+
+// Natural-log LSE of a row with base-2 maximum m2 and sum l of 2^(s - m2).
+__device__ __forceinline__ float lse_natural(float m2, float l) {
+    return l > 0.f ? (m2 + log2f(l)) * 0.6931471805599453f : -CUDART_INF_F;
+}
 
 // Rows at or beyond the sequence length hold no cached token: zero `nchunks`
 // SW128 chunks of 64 keys from row r0 on (one warp), so that masked rows can
@@ -720,9 +726,13 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                 rl[kh * kHeads + m] = l_part;
                 named_bar_sync(1 + quarter, 64);
                 const float l_sum = rl[m] + rl[kHeads + m];
-                if (ok && !w.whole && kh == 0) {
-                    const size_t pslot = (size_t)(grp + w.seq) * q_len + qi;
-                    args.part_lse[pslot * kHeads + m] = l_sum > 0.f ? m_used + __log2f(l_sum) : -CUDART_INF_F;
+                if (ok && kh == 0 && (!w.whole || args.lse)) {
+                    if (w.whole) {
+                        args.lse[((size_t)w.seq * q_len + qi) * kHeads + m] = lse_natural(m_used, l_sum);
+                    } else {
+                        const size_t pslot = (size_t)(grp + w.seq) * q_len + qi;
+                        args.part_lse[pslot * kHeads + m] = l_sum > 0.f ? m_used + __log2f(l_sum) : -CUDART_INF_F;
+                    }
                 }
                 m_used = -CUDART_INF_F;
                 l_part = 0.f;
@@ -1028,8 +1038,14 @@ __device__ __forceinline__ void mla_plan_warp(const int32_t* __restrict__ seqlen
 
 __global__ void __launch_bounds__(32) mla_plan_kernel(const int32_t* __restrict__ seqlens, int B, int q_len,
                                                       int T_max, int clusters, int ovh, int min_units, Plan* plan,
-                                                      int* status, __nv_bfloat16* o_lat) {
+                                                      int* status, __nv_bfloat16* o_lat, float* lse) {
     mla_plan_warp(seqlens, B, q_len, T_max, clusters, ovh, min_units, plan, status, o_lat, threadIdx.x);
+    if (!lse) return;
+    for (int b = 0; b < B; ++b) {
+        const int T = seqlens[b];
+        if (T >= q_len && T <= T_max) continue;
+        for (int i = threadIdx.x; i < q_len * kHeads; i += 32) lse[(size_t)b * q_len * kHeads + i] = -CUDART_INF_F;
+    }
 }
 
 // ------------------------------------------------------------------ combine
@@ -1137,7 +1153,8 @@ __device__ __forceinline__ void merge_pieces_warp(const UnitPieces& up, int b, i
 __global__ void __launch_bounds__(256) mla_combine_kernel(const Plan* __restrict__ plan,
                                                           const float* __restrict__ part_o,
                                                           const float* __restrict__ part_lse,
-                                                          __nv_bfloat16* __restrict__ o_lat) {
+                                                          __nv_bfloat16* __restrict__ o_lat,
+                                                          float* __restrict__ lse) {
     MLA_KT(kKtCombine, 0);
     pdl_wait();
     pdl_trigger();
@@ -1157,6 +1174,7 @@ __global__ void __launch_bounds__(256) mla_combine_kernel(const Plan* __restrict
     MergeState ms;
     ms.clear();
     merge_pieces_warp(up, b, qi, q_len, h, part_o, part_lse, lane, 0, 1, ms);
+    if (lse && lane == 0) lse[(size_t)(b * q_len + qi) * kHeads + h] = lse_natural(ms.m, ms.wsum);
     ms.normalise();
     uint2* dst = reinterpret_cast<uint2*>(o_lat + ((size_t)(b * q_len + qi) * kHeads + h) * kLat) + lane;
 #pragma unroll
