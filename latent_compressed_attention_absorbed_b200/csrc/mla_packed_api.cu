@@ -81,9 +81,11 @@ int write_rows(const mla_dims_t* dims, bool packed, const void* c_kv, const void
 }
 
 struct PackedDecodeLayout {
-    size_t q_hat, o_lat, total;
+    size_t q_hat, o_lat, attend, total;
 };
 
+// The tensor-core attention's part is always counted where it can run, so that
+// one size serves every option.
 PackedDecodeLayout packed_decode_layout(const Problem& p) {
     Carve c(nullptr);
     PackedDecodeLayout L;
@@ -92,6 +94,8 @@ PackedDecodeLayout packed_decode_layout(const Problem& p) {
     c.take(U * (p.d_c + p.d_r) * elem_size(p));
     L.o_lat = c.off;
     c.take(U * p.d_c * elem_size(p));
+    L.attend = c.off;
+    if (sm100_supported(p, p.q_len)) c.take(sm100_attend_workspace_bytes(p, sm100_default_pairs()) + kWsAlign);
     L.total = c.off;
     return L;
 }
@@ -174,7 +178,17 @@ int mla_attend_packed(const mla_dims_t* dims, const void* q_hat, const mla_cache
     if (rc) return rc;
     int* status = device_status_ptr();
     if (!status) return set_error(MLA_ERR_CUDA, "no CUDA device / status word");
-    return cuda_error(generic_attend_rows(p, true, q_hat, cv, seqlens, o_lat, lse, status, (cudaStream_t)stream),
+    if (!fast)
+        return cuda_error(generic_attend_rows(p, true, q_hat, cv, seqlens, o_lat, lse, status, (cudaStream_t)stream),
+                          "packed attend launch");
+    const int pairs = pairs_for(opts);
+    const size_t need = sm100_attend_workspace_bytes(p, pairs) + kWsAlign;
+    if (!workspace || workspace_bytes < need || !aligned16(workspace))
+        return set_error(MLA_ERR_WORKSPACE, "packed attend workspace needs %zu bytes (16-byte aligned), got %zu", need,
+                         workspace_bytes);
+    workspace = align_ws(workspace, &workspace_bytes);
+    return cuda_error(sm100_attend_packed(p, q_hat, cv, seqlens, o_lat, lse, workspace, workspace_bytes, pairs, status, opts,
+                                          (cudaStream_t)stream),
                       "packed attend launch");
 }
 
@@ -205,7 +219,7 @@ int mla_decode_packed(const mla_dims_t* dims, const void* q_nope, const void* q_
     void* o_lat = ws + L.o_lat;
     rc = mla_absorb_query(dims, q_nope, q_rope, W_UK, n_seen ? n_seen : seqlens, B, q_len, qh, opts, stream);
     if (rc) return rc;
-    rc = mla_attend_packed(dims, qh, cache, seqlens, B, q_len, o_lat, lse, ws + L.total, workspace_bytes - L.total, opts,
+    rc = mla_attend_packed(dims, qh, cache, seqlens, B, q_len, o_lat, lse, ws + L.attend, L.total - L.attend, opts,
                            stream);
     if (rc) return rc;
     return mla_project_out(dims, o_lat, W_UV, B * q_len, out, opts, stream);

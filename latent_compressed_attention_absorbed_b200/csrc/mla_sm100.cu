@@ -14,6 +14,8 @@
 #include "sm100_attend.cuh"
 #include "sm100_gemm.cuh"
 #include "sm100_gemv.cuh"
+#include "sm100_packed_attend.cuh"
+#include "mla_packed_internal.h"
 
 #ifdef MLA_TRACE
 // Copies the attention kernel's timing trace (4096 tiles x 16 stamps) to host
@@ -80,7 +82,7 @@ __global__ void append_v3_kernel(const __nv_bfloat16* __restrict__ c_kv, const _
     MLA_KT(kKtAppend, 2);
 }
 
-bool g_smem_absorb[kMaxDev], g_smem_project[kMaxDev], g_smem_attend[kMaxDev];
+bool g_smem_absorb[kMaxDev], g_smem_project[kMaxDev], g_smem_attend[kMaxDev], g_smem_packed[kMaxDev];
 bool g_smem_absorb_gemv[4][kMaxDev], g_smem_project_gemv[4][kMaxDev];
 
 constexpr int kAbsorbStages = 2;
@@ -299,7 +301,7 @@ cudaError_t sm100_attend(const Problem& p, const void* q_hat, const CacheView& c
 
     cudaError_t e;
     if (!plan_ready) {
-        mla_plan_kernel<<<1, 32, 0, st>>>(seqlens, p.B, p.q_len, cache.T_max, clusters, plan_ovh(overhead_tiles),
+        mla_plan_kernel<kNk><<<1, 32, 0, st>>>(seqlens, p.B, p.q_len, cache.T_max, clusters, plan_ovh(overhead_tiles),
                                           plan_min_units(min_tiles), plan, status, (__nv_bfloat16*)o_lat, lse);
         e = cudaGetLastError();
         if (e != cudaSuccess) return e;
@@ -342,6 +344,52 @@ cudaError_t sm100_attend(const Problem& p, const void* q_hat, const CacheView& c
                        (const float*)a.part_o, (const float*)a.part_lse, (__nv_bfloat16*)o_lat, lse);
     if (e != cudaSuccess) return e;
     return cudaGetLastError();
+}
+
+cudaError_t sm100_attend_packed(const Problem& p, const void* q_hat, const CacheView& cache, const int32_t* seqlens,
+                                void* o_lat, float* lse, void* workspace, size_t ws_bytes, int num_pairs, int* status,
+                                const mla_decode_opts_t* opts, cudaStream_t st) {
+    const int clusters = attend_clusters(num_pairs, p.q_len);
+    if (clusters / p.q_len > kPlanMaxGroups) return cudaErrorInvalidValue;
+    size_t off_part, off_lse;
+    if (ws_bytes < attend_layout(p, clusters, &off_part, &off_lse)) return cudaErrorInvalidValue;
+    char* ws = static_cast<char*>(workspace);
+    Plan* plan = reinterpret_cast<Plan*>(ws);
+    CUtensorMap mRaw, mRope;
+    const uint64_t stt = (uint64_t)cache.stride_t;
+    const uint64_t sb = p.B > 1 ? (uint64_t)cache.stride_b : stt * (uint64_t)cache.T_max;
+    const uint8_t* rows = static_cast<const uint8_t*>(cache.data);
+    if (!make_map_words(&mRaw, rows, pk::kRawRow / 2, cache.T_max, p.B, stt, sb, pk::kRawRow / 2, pk::kUnit, 1,
+                        CU_TENSOR_MAP_SWIZZLE_NONE) ||
+        !make_map(&mRope, rows + kPackRope, kRope, cache.T_max, p.B, stt, sb, kRope, pk::kUnit, 1, CU_TENSOR_MAP_SWIZZLE_128B))
+        return cudaErrorInvalidValue;
+    mla_plan_kernel<pk::kTile><<<1, 32, 0, st>>>(seqlens, p.B, p.q_len, cache.T_max, clusters,
+                                                 opts && opts->overhead_tiles >= 0 ? opts->overhead_tiles : 1,
+                                                 opts && opts->min_tiles > 0 ? opts->min_tiles : 1, plan, status,
+                                                 (__nv_bfloat16*)o_lat, lse);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    e = set_smem(pk::packed_attend_kernel, pk::kSmem, g_smem_packed);
+    if (e != cudaSuccess) return e;
+    pk::Args a;
+    a.plan = plan;
+    a.seqlens = seqlens;
+    a.q_len = p.q_len;
+    a.scale_log2 = p.scale * 1.4426950408889634f;
+    a.q_hat = (const __nv_bfloat16*)q_hat;
+    a.o_lat = (__nv_bfloat16*)o_lat;
+    a.o_lat_v8 = (reinterpret_cast<uintptr_t>(o_lat) & 31u) == 0;
+    a.part_o = reinterpret_cast<float*>(ws + off_part);
+    a.part_lse = reinterpret_cast<float*>(ws + off_lse);
+    a.lse = lse;
+    a.status = status;
+    a.wait_limit_ns = (opts && opts->wait_limit_ns > 0) ? (uint64_t)opts->wait_limit_ns : MLA_WAIT_LIMIT_NS;
+    e = launch_pdl(pk::packed_attend_kernel, dim3(clusters * 2), dim3(pk::kThreads), pk::kSmem, st, 2, mRaw, mRope, a);
+    if (e != cudaSuccess) return e;
+    const int units = p.B * p.q_len;
+    const int max_split = units < clusters ? units : clusters;
+    return launch_pdl(mla_combine_kernel, dim3(max_split * (kHeads / 8)), dim3(256), 0, st, 1, (const Plan*)plan,
+                      (const float*)a.part_o, (const float*)a.part_lse, (__nv_bfloat16*)o_lat, lse);
 }
 
 cudaError_t sm100_project_small(const Problem& p, void* attend_workspace, int num_pairs, const void* o_lat,

@@ -951,11 +951,12 @@ __global__ void __launch_bounds__(kAttThreads, 1)
 
 // ------------------------------------------------------------------ plan
 
-// Per sequence: cost_b = ceil(T_b / 64) + ovh (0 for an invalid length);
+// Per sequence: cost_b = ceil(T_b / kTile) + ovh (0 for an invalid length);
 // prefix sums, the per-group share L = ceil(total / groups) (at least
 // min_units), the list of sequences cut across groups, and o_lat = 0 for the
 // tokens of sequences with an invalid length (their decode has no defined
 // result).  One warp.
+template <int kTile = kNk>
 __device__ __forceinline__ void mla_plan_warp(const int32_t* __restrict__ seqlens, int B, int q_len, int T_max,
                                               int clusters, int ovh, int min_units, Plan* plan, int* status,
                                               __nv_bfloat16* o_lat, int lane) {
@@ -972,7 +973,7 @@ __device__ __forceinline__ void mla_plan_warp(const int32_t* __restrict__ seqlen
         if (b < B) {
             const int T = seqlens[b];
             if (T < q_len || T > T_max) atomicOr(status, MLA_STATUS_BAD_SEQLEN);
-            else c = (T + kNk - 1) / kNk + ovh;
+            else c = (T + kTile - 1) / kTile + ovh;
             c_min = min(c_min, c);
             c_max = max(c_max, c);
         }
@@ -1036,10 +1037,11 @@ __device__ __forceinline__ void mla_plan_warp(const int32_t* __restrict__ seqlen
     }
 }
 
+template <int kTile>
 __global__ void __launch_bounds__(32) mla_plan_kernel(const int32_t* __restrict__ seqlens, int B, int q_len,
                                                       int T_max, int clusters, int ovh, int min_units, Plan* plan,
                                                       int* status, __nv_bfloat16* o_lat, float* lse) {
-    mla_plan_warp(seqlens, B, q_len, T_max, clusters, ovh, min_units, plan, status, o_lat, threadIdx.x);
+    mla_plan_warp<kTile>(seqlens, B, q_len, T_max, clusters, ovh, min_units, plan, status, o_lat, threadIdx.x);
     if (!lse) return;
     for (int b = 0; b < B; ++b) {
         const int T = seqlens[b];

@@ -118,6 +118,27 @@ __device__ __forceinline__ bool warp_wait_cluster(uint32_t bar, uint32_t parity,
     return __all_sync(0xffffffffu, mbar_wait_cluster(bar, parity, limit_ns));
 }
 
+// The whole-warp form as a function of its own: for kernels whose roles would
+// otherwise not fit the instruction cache (one copy of the spin loop serves
+// every wait).  Acquires at cluster scope, so it serves barriers completed by
+// either CTA of a pair.
+static __device__ __noinline__ bool warp_wait_shared(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
+    uint64_t t0 = 0;
+    bool ok = true;
+#pragma unroll 1
+    for (uint32_t i = 1; !mbar_try_wait_cluster(bar, parity); ++i) {
+        if ((i & 63) == 0) {
+            const uint64_t now = global_timer_ns();
+            if (t0 == 0) t0 = now;
+            else if (now - t0 > limit_ns) {
+                ok = false;
+                break;
+            }
+        }
+    }
+    return __all_sync(0xffffffffu, ok);
+}
+
 // Spins for `ns` nanoseconds of the global timer (bounded by construction).
 __device__ __forceinline__ void spin_ns(uint64_t ns) {
     const uint64_t t0 = global_timer_ns();
@@ -275,6 +296,14 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uin
         : "memory");
 }
 
+// One lane of a converged warp, always the same one; the compiler knows the
+// branch to be uniform and keeps descriptors in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
 // Arrive once on `bar` when all previously issued tcgen05.mma of this thread complete.
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
@@ -307,6 +336,11 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
         "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]),
         "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
         : "memory");
+}
+
+// One 32-bit column of each thread's own lane.
+__device__ __forceinline__ void tmem_st1(uint32_t taddr, uint32_t v) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "r"(v));
 }
 
 // Each thread of the warp reads 16 consecutive 32-bit columns of its own lane.
@@ -358,6 +392,11 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N, bool a_mn, b
            | ((b_mn ? 1u : 0u) << 16)     // B major
            | ((uint32_t)(N >> 3) << 17)   // N >> 3
            | ((uint32_t)(M >> 4) << 24);  // M >> 4
+}
+
+// The same with fp16 A and B.
+__host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool a_mn, bool b_mn) {
+    return idesc_bf16_f32(M, N, a_mn, b_mn) & ~((1u << 7) | (1u << 10));
 }
 
 // ------------------------------------------------------------------ programmatic dependent launch

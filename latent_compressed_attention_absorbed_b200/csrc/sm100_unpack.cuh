@@ -1,0 +1,89 @@
+// Packed 4-bit rows in registers: sixteen latents of a group as eight pairs of
+// bf16 or fp16 values, exactly (the format is described in mla_packed.cuh).
+#pragma once
+
+#include <stdint.h>
+
+#include "mla_packed.cuh"
+#include "sm100_ptx.cuh"
+
+namespace mla {
+namespace sm100 {
+
+constexpr int kPackNib = 256;    // bytes of codes of a V3 row
+constexpr int kPackScale = 32;   // bytes of scales
+constexpr int kPackRope = 288;   // where its key starts
+constexpr int kPackRow = 416;
+
+__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t r;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+    return r;
+}
+__device__ __forceinline__ uint32_t fma_f16x2(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t r;
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t ld_shared_u32(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+// Pairs 0..7 of a group from its two words and its scale byte.  A code moved
+// to the top of the fraction of 16.0 reads 16 + n; one fused multiply-add
+// with the scale gives (16 + n) s - 24 s = q s: two shifts' worth of integer
+// work and one floating-point instruction for two values.
+template <bool kF16>
+__device__ __forceinline__ void unpack16(uint32_t w0, uint32_t w1, uint32_t scale_byte, uint32_t (&out)[8]) {
+    const float s = packed_scale(scale_byte);
+    if constexpr (kF16) {
+        const uint32_t s2 = pack_f16(s, s), c2 = pack_f16(-24.0f * s, -24.0f * s);
+        constexpr uint32_t kMask = 0x03C003C0u, kOne = 0x4C004C00u;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t w = h ? w1 : w0;
+            out[4 * h + 0] = fma_f16x2(((w << 6) & kMask) | kOne, s2, c2);
+            out[4 * h + 1] = fma_f16x2(((w << 2) & kMask) | kOne, s2, c2);
+            out[4 * h + 2] = fma_f16x2(((w >> 2) & kMask) | kOne, s2, c2);
+            out[4 * h + 3] = fma_f16x2(((w >> 6) & kMask) | kOne, s2, c2);
+        }
+    } else {
+        const uint32_t s2 = pack_bf16(s, s), c2 = pack_bf16(-24.0f * s, -24.0f * s);
+        constexpr uint32_t kMask = 0x00780078u, kOne = 0x41804180u;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t w = h ? w1 : w0;
+            out[4 * h + 0] = fma_bf16x2(((w << 3) & kMask) | kOne, s2, c2);
+            out[4 * h + 1] = fma_bf16x2(((w >> 1) & kMask) | kOne, s2, c2);
+            out[4 * h + 2] = fma_bf16x2(((w >> 5) & kMask) | kOne, s2, c2);
+            out[4 * h + 3] = fma_bf16x2(((w >> 9) & kMask) | kOne, s2, c2);
+        }
+    }
+}
+
+// One row's 64 latents of chunk c of a raw row in shared memory (32 bytes of
+// codes, four scale bytes) -> 128 bytes of values at row `row` of a swizzled
+// chunk of 128-byte rows.  Two groups at a time: a short loop, as the roles
+// that run beside this one share the instruction cache.
+template <bool kF16>
+__device__ __forceinline__ void unpack_chunk_row(uint32_t raw_row, int c, uint32_t chunk_row, int row) {
+    uint32_t scales = ld_shared_u32(raw_row + kPackNib + 4 * c);
+#pragma unroll 1
+    for (int h = 0; h < 2; ++h) {
+        uint32_t w[4], v[8];
+        ld_shared_v4u(raw_row + 32 * c + 16 * h, w[0], w[1], w[2], w[3]);
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+            unpack16<kF16>(w[2 * g], w[2 * g + 1], scales & 0xFFu, v);
+            scales >>= 8;
+            st_shared_v4(chunk_row + (((4 * h + 2 * g) ^ (row & 7)) << 4), v[0], v[1], v[2], v[3]);
+            st_shared_v4(chunk_row + (((4 * h + 2 * g + 1) ^ (row & 7)) << 4), v[4], v[5], v[6], v[7]);
+        }
+    }
+}
+
+}  // namespace sm100
+}  // namespace mla
