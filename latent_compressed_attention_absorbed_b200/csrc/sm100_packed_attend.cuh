@@ -290,11 +290,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int st = g % kRawStages;
                 if (!wait(kRawFull + st, g / kRawStages) || *abort_flag) { ok = false; break; }
                 const uint32_t src = base + st * kRawBytes + row * kRawRow;
+                RawChunk raw;
+                raw.load(src, odd);
 #pragma unroll 1
                 for (int c = odd; c < 8; c += 2) {
                     const int slot = c % kChunks;
                     if (!wait(kChEmpty + slot, c / kChunks + 1)) { ok = false; break; }
-                    unpack_chunk_row<false>(src, c, base + kOffChunk + slot * kChunkBytes + row * 128, row);
+                    raw.unpack<false>(base + kOffChunk + slot * kChunkBytes + row * 128, row);
+                    if (c + 2 < 8) raw.load(src, c + 2);
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) {
@@ -506,11 +509,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
             for (; u < u1; ++u) {
                 const int st = u % kARawStages, vs = u % kVStages;
-                if (!wait(kARawFull + st, u / kARawStages) || !wait(kVEmpty + vs, u / kVStages + 1) || *abort_flag) { ok = false; break; }
+                if (!wait(kARawFull + st, u / kARawStages) || *abort_flag) { ok = false; break; }
                 const uint32_t src = base + st * kARawBytes + row * kRawRow;
-#pragma unroll 1
-                for (int c = 2 * part; c < 2 * part + 2; ++c)
-                    unpack_chunk_row<true>(src, c, base + kOffV + vs * kVBytes + c * kVChunk + row * 128, row);
+                RawChunk raw;
+                raw.load(src, 2 * part);
+                if (!wait(kVEmpty + vs, u / kVStages + 1)) { ok = false; break; }
+                const uint32_t dst = base + kOffV + vs * kVBytes + 2 * part * kVChunk + row * 128;
+                raw.unpack<true>(dst, row);
+                raw.load(src, 2 * part + 1);
+                raw.unpack<true>(dst + kVChunk, row);
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {

@@ -64,26 +64,26 @@ __device__ __forceinline__ void unpack16(uint32_t w0, uint32_t w1, uint32_t scal
     }
 }
 
-// One row's 64 latents of chunk c of a raw row in shared memory (32 bytes of
-// codes, four scale bytes) -> 128 bytes of values at row `row` of a swizzled
-// chunk of 128-byte rows.  Two groups at a time: a short loop, as the roles
-// that run beside this one share the instruction cache.
-template <bool kF16>
-__device__ __forceinline__ void unpack_chunk_row(uint32_t raw_row, int c, uint32_t chunk_row, int row) {
-    uint32_t scales = ld_shared_u32(raw_row + kPackNib + 4 * c);
-#pragma unroll 1
-    for (int h = 0; h < 2; ++h) {
-        uint32_t w[4], v[8];
-        ld_shared_v4u(raw_row + 32 * c + 16 * h, w[0], w[1], w[2], w[3]);
+// The codes and scales of 64 latents (chunk c) of a raw row in shared memory.
+struct RawChunk {
+    uint32_t w[8], scales;
+    __device__ __forceinline__ void load(uint32_t raw_row, int c) {
+        scales = ld_shared_u32(raw_row + kPackNib + 4 * c);
+        ld_shared_v4u(raw_row + 32 * c, w[0], w[1], w[2], w[3]);
+        ld_shared_v4u(raw_row + 32 * c + 16, w[4], w[5], w[6], w[7]);
+    }
+    // -> 128 bytes of values at row `row` of a swizzled chunk of 128-byte rows
+    template <bool kF16>
+    __device__ __forceinline__ void unpack(uint32_t chunk_row, int row) const {
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
-            unpack16<kF16>(w[2 * g], w[2 * g + 1], scales & 0xFFu, v);
-            scales >>= 8;
-            st_shared_v4(chunk_row + (((4 * h + 2 * g) ^ (row & 7)) << 4), v[0], v[1], v[2], v[3]);
-            st_shared_v4(chunk_row + (((4 * h + 2 * g + 1) ^ (row & 7)) << 4), v[4], v[5], v[6], v[7]);
+        for (int g = 0; g < 4; ++g) {
+            uint32_t v[8];
+            unpack16<kF16>(w[2 * g], w[2 * g + 1], (scales >> (8 * g)) & 0xFFu, v);
+            st_shared_v4(chunk_row + (((2 * g) ^ (row & 7)) << 4), v[0], v[1], v[2], v[3]);
+            st_shared_v4(chunk_row + (((2 * g + 1) ^ (row & 7)) << 4), v[4], v[5], v[6], v[7]);
         }
     }
-}
+};
 
 }  // namespace sm100
 }  // namespace mla
