@@ -280,6 +280,10 @@ int mla_accumulate_weights(const mla_dims_t* dims, const void* q_hat, const floa
     if (rc) return rc;
     int* status = device_status_ptr();
     if (!status) return set_error(MLA_ERR_CUDA, "no CUDA device / status word");
+    if (fast)
+        return cuda_error(sm100_weights(p, cache_format == MLA_CACHE_PACKED, q_hat, lse, cv, seqlens, decay, prev, weights,
+                                        weights_stride, status, opts, (cudaStream_t)stream),
+                          "weights launch");
     return cuda_error(generic_weights(p, cache_format == MLA_CACHE_PACKED, q_hat, lse, cv, seqlens, decay, prev, weights,
                                       weights_stride, status, (cudaStream_t)stream),
                       "weights launch");

@@ -25,6 +25,10 @@ cudaError_t sm100_attend_packed(const Problem& p, const void* q_hat, const Cache
                                 void* o_lat, float* lse, void* workspace, size_t ws_bytes, int num_pairs, int* status,
                                 const mla_decode_opts_t* opts, cudaStream_t st);
 
+cudaError_t sm100_weights(const Problem& p, bool packed, const void* q_hat, const float* lse, const CacheView& cache,
+                          const int32_t* seqlens, float decay, const float* prev, float* weights, int64_t stride_w,
+                          int* status, const mla_decode_opts_t* opts, cudaStream_t st);
+
 // Eviction: which rows stay, and the compaction.
 struct EvictArgs {
     int B, T_max, budget, n_sink, n_recent;

@@ -15,6 +15,7 @@
 #include "sm100_gemm.cuh"
 #include "sm100_gemv.cuh"
 #include "sm100_packed_attend.cuh"
+#include "sm100_weights.cuh"
 #include "mla_packed_internal.h"
 
 #ifdef MLA_TRACE
@@ -83,6 +84,7 @@ __global__ void append_v3_kernel(const __nv_bfloat16* __restrict__ c_kv, const _
 }
 
 bool g_smem_absorb[kMaxDev], g_smem_project[kMaxDev], g_smem_attend[kMaxDev], g_smem_packed[kMaxDev];
+bool g_smem_weights[2][kMaxDev];
 bool g_smem_absorb_gemv[4][kMaxDev], g_smem_project_gemv[4][kMaxDev];
 
 constexpr int kAbsorbStages = 2;
@@ -390,6 +392,52 @@ cudaError_t sm100_attend_packed(const Problem& p, const void* q_hat, const Cache
     const int max_split = units < clusters ? units : clusters;
     return launch_pdl(mla_combine_kernel, dim3(max_split * (kHeads / 8)), dim3(256), 0, st, 1, (const Plan*)plan,
                       (const float*)a.part_o, (const float*)a.part_lse, (__nv_bfloat16*)o_lat, lse);
+}
+
+template <bool kPacked>
+static cudaError_t weights_launch(const CUtensorMap& mQ, const CUtensorMap& mRows, const CUtensorMap& mKey, const wt::Args& a,
+                                  cudaStream_t st) {
+    using C = wt::Cfg<kPacked>;
+    cudaError_t e = set_smem(wt::weights_kernel<kPacked>, C::kSmem, g_smem_weights[kPacked]);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(wt::weights_kernel<kPacked>, dim3(device_sm_count()), dim3(C::kThreads), C::kSmem, st, 1, mQ, mRows, mKey, a);
+}
+
+cudaError_t sm100_weights(const Problem& p, bool packed, const void* q_hat, const float* lse, const CacheView& cache,
+                          const int32_t* seqlens, float decay, const float* prev, float* weights, int64_t stride_w,
+                          int* status, const mla_decode_opts_t* opts, cudaStream_t st) {
+    CUtensorMap mQ, mRows, mKey;
+    if (!make_map(&mQ, q_hat, kRow, kHeads, (uint64_t)p.B * p.q_len, kRow * 2, (uint64_t)kHeads * kRow * 2, 64, kHeads, 1,
+                  CU_TENSOR_MAP_SWIZZLE_128B))
+        return cudaErrorInvalidValue;
+    const uint64_t es = packed ? 1 : 2;
+    const uint64_t stt = (uint64_t)cache.stride_t * es;
+    const uint64_t sb = p.B > 1 ? (uint64_t)cache.stride_b * es : stt * (uint64_t)cache.T_max;
+    const uint8_t* rows = static_cast<const uint8_t*>(cache.data);
+    bool made;
+    if (packed) {
+        made = make_map_words(&mRows, rows, wt::kRawRow / 2, cache.T_max, p.B, stt, sb, wt::kRawRow / 2, wt::kUnit, 1,
+                              CU_TENSOR_MAP_SWIZZLE_NONE) &&
+               make_map(&mKey, rows + kPackRope, kRope, cache.T_max, p.B, stt, sb, kRope, wt::kUnit, 1, CU_TENSOR_MAP_SWIZZLE_128B);
+    } else {
+        made = make_map(&mRows, rows, kRow, cache.T_max, p.B, stt, sb, 64, wt::kTile, 1, CU_TENSOR_MAP_SWIZZLE_128B);
+        mKey = mRows;
+    }
+    if (!made) return cudaErrorInvalidValue;
+    wt::Args a;
+    a.seqlens = seqlens;
+    a.lse = lse;
+    a.prev = prev;
+    a.weights = weights;
+    a.stride_w = stride_w;
+    a.decay = decay;
+    a.scale_log2 = p.scale * 1.4426950408889634f;
+    a.B = p.B;
+    a.q_len = p.q_len;
+    a.T_max = cache.T_max;
+    a.status = status;
+    a.wait_limit_ns = (opts && opts->wait_limit_ns > 0) ? (uint64_t)opts->wait_limit_ns : MLA_WAIT_LIMIT_NS;
+    return packed ? weights_launch<true>(mQ, mRows, mKey, a, st) : weights_launch<false>(mQ, mRows, mKey, a, st);
 }
 
 cudaError_t sm100_project_small(const Problem& p, void* attend_workspace, int num_pairs, const void* o_lat,

@@ -1,0 +1,460 @@
+// Accumulated attention weights on tcgen05 / TMEM:
+//   w_t = sum over queries i and heads h of exp(scale * q_hat_ih . row_t - lse_ih)
+// for every cached row t of a sequence, added to decay * prev_t.
+//
+// The rows are the M dimension here: S^T = rows . Q-hat^T has one row of the
+// cache in each TMEM lane and the 128 heads in its columns, so a thread sums
+// the weights of its own row and nothing is exchanged between lanes, and the
+// result needs no atomics.  Q-hat of one query token (144 KB) stays in shared
+// memory as the B operand; the rows stream past it:
+//   full-width rows: TMA fills a ring of 128 x 64 chunks, the A operand;
+//   packed rows: TMA brings the raw rows, eight warps unpack them to bf16 and
+//     store them straight into TMEM, from where the products read their A
+//     operand (eight chunks of 32 columns: one tile), so unpacked rows cost no
+//     shared-memory bandwidth; the keys are a shared-memory A operand.
+// Bound: 128 flop a byte for full-width rows: HBM (3.3 us a 128-row tile and
+// SM against 1.4 us of products); 354 for packed rows: the tensor cores.
+//
+// Split.  The tiles of all sequences are cut into equal ranges, one CTA an SM;
+// a tile is one CTA's for all queries, so a row's sum is always formed in the
+// same order.  With several queries a CTA goes through its range in blocks of
+// eight tiles, query by query, so that the rows' second and later readings
+// come from L2; the sums of a block wait in shared memory.  Two sets of four
+// warps take alternate tiles of a block.
+//
+// Every wait is bounded; no warp waits on a barrier without a limit before
+// the common end, so a wait that expires ends the kernel in order.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <math_constants.h>
+
+#include "sm100_attend.cuh"
+#include "sm100_unpack.cuh"
+
+namespace mla {
+namespace sm100 {
+namespace wt {
+
+constexpr int kTile = 128;                // rows of a tile
+constexpr int kUnit = 64;                 // rows of a raw copy
+constexpr int kChunkBytes = kTile * 128;  // 128 rows x 64 bf16, SW128
+constexpr int kQChunks = 9;
+constexpr int kBlock = 8;                 // tiles of a block when there are several queries
+constexpr int kRawRow = kPackNib + kPackScale;
+constexpr int kRawBytes = kUnit * kRawRow;  // 18 KB: 64 raw rows
+constexpr int kSetWarps = 4;
+
+template <bool kPacked>
+struct Cfg {
+    static constexpr int kThreads = kPacked ? 640 : 384;
+    static constexpr int kRing = kPacked ? 8 : 4;  // chunks: TMEM columns / shared memory
+    static constexpr int kRawStages = 3;
+    static constexpr int kOffRing = kQChunks * kChunkBytes;
+    // packed: the keys' chunk, then the raw stages; full width: the ring
+    static constexpr int kOffRaw = kOffRing + kChunkBytes;
+    static constexpr int kOffSums = kPacked ? kOffRaw + kRawStages * kRawBytes : kOffRing + kRing * kChunkBytes;
+    static constexpr int kOffLse = kOffSums + kBlock * kTile * 4;   // [8 warps][128]
+    static constexpr int kOffBars = kOffLse + 2 * kSetWarps * kHeads * 4;
+    static constexpr int kSmem = kOffBars + 512 + 1024;
+    static_assert(kSmem <= 232448, "shared memory exceeds 227 KB");
+    static_assert(kOffRaw % 1024 == 0, "alignment");
+    // barriers
+    enum {
+        kQFull = 0,                    // Q-hat chunk loaded (tx)
+        kQEmpty = kQFull + kQChunks,   // Q-hat chunk of the previous query multiplied (MMA commit)
+        kChFull = kQEmpty + kQChunks,  // ring chunk in place (tx, or 4 warps)
+        kChEmpty = kChFull + kRing,    // ring chunk multiplied (MMA commit)
+        kSFull = kChEmpty + kRing,     // S of a set complete (MMA commit)
+        kSFree = kSFull + 2,           // S of a set read (4 warps)
+        kRawFull = kSFree + 2,         // raw rows loaded (tx)
+        kRawEmpty = kRawFull + kRawStages,  // raw rows unpacked (2 row quarters x 2 warps)
+        kKeyFull = kRawEmpty + kRawStages,  // keys loaded (tx)
+        kKeyEmpty,                          // keys multiplied (MMA commit)
+        kDrain,
+        kBars
+    };
+    static_assert(8 * (kBars + 2) <= 480, "barrier block too small");
+};
+constexpr int kTmemS = 0;       // two buffers of 128 fp32 columns
+constexpr int kTmemRing = 256;  // packed: eight chunks of 32 columns
+
+struct Args {
+    const int32_t* seqlens;
+    const float* lse;   // [B][q_len][128]
+    const float* prev;  // or NULL
+    float* weights;
+    int64_t stride_w;
+    float decay, scale_log2;
+    int B, q_len, T_max;
+    int* status;
+    uint64_t wait_limit_ns;
+};
+
+// The tile ranges of a CTA: every sequence costs its tiles and one more (its
+// Q-hat); the CTA's share is units lo..hi-1 of that list.
+struct Pieces {
+    const int32_t* seqlens;
+    int B, q_len, T_max, lo, hi, pre, b;
+    static __device__ __forceinline__ int cost(int T, int q_len, int T_max) {
+        return T < q_len || T > T_max ? 0 : (T + kTile - 1) / kTile + 1;
+    }
+    __device__ bool next(int& seq, int& T, int& k0, int& k1) {
+        while (b < B && pre < hi) {
+            const int len = seqlens[b], c = cost(len, q_len, T_max);
+            int s = lo - pre - 1, e = hi - pre - 1;
+            s = s < 0 ? 0 : s;
+            e = e > c - 1 ? c - 1 : e;
+            const int cur = b++;
+            pre += c;
+            if (e > s) {
+                seq = cur;
+                T = len;
+                k0 = s;
+                k1 = e;
+                return true;
+            }
+        }
+        return false;
+    }
+};
+
+// Share of every CTA and the sequence this one starts in (all threads; two
+// block barriers).  plan: {units a CTA, first sequence, its first unit}.
+__device__ __forceinline__ void plan_pieces(const Args& a, int* plan, int* scratch, Pieces& p) {
+    const int n = blockDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int per = (a.B + n - 1) / n;
+    const int b0 = tid * per;
+    int sum = 0;
+    bool bad = false;
+    for (int b = b0; b < b0 + per && b < a.B; ++b) {
+        const int c = Pieces::cost(a.seqlens[b], a.q_len, a.T_max);
+        bad |= c == 0;
+        sum += c;
+    }
+    if (bad && blockIdx.x == 0) atomicOr(a.status, MLA_STATUS_BAD_SEQLEN);
+    int inc = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += y;
+    }
+    if (lane == 31) scratch[warp] = inc;
+    if (tid == 0) plan[1] = a.B;
+    __syncthreads();
+    int before = 0, total = 0;
+    for (int w = 0; w < n / 32; ++w) {
+        const int s = scratch[w];
+        if (w < warp) before += s;
+        total += s;
+    }
+    const int share = (total + gridDim.x - 1) / gridDim.x;
+    const int lo = blockIdx.x * share;
+    int pre = before + inc - sum;
+    if (lo >= pre && lo < pre + sum) {
+        int b = b0;
+        for (;; ++b) {
+            const int c = Pieces::cost(a.seqlens[b], a.q_len, a.T_max);
+            if (lo < pre + c) break;
+            pre += c;
+        }
+        plan[1] = b;
+        plan[2] = pre;
+    }
+    __syncthreads();
+    p.seqlens = a.seqlens;
+    p.B = a.B;
+    p.q_len = a.q_len;
+    p.T_max = a.T_max;
+    p.lo = lo;
+    p.hi = lo + share;
+    p.b = plan[1];
+    p.pre = p.b < a.B ? plan[2] : 0;
+}
+
+// mapQ: Q-hat [tokens][128 heads][576], box 64 x 128 x 1, SW128.
+// full width: mapRows [B][T_max][576], box 64 x 128 rows, SW128 (mapKey unused);
+// packed: mapRows the codes and scales [B][T_max][144 words], box 144 x 64 rows; mapKey the keys, box 64 x 64 rows, SW128.
+template <bool kPacked>
+__global__ void __launch_bounds__(Cfg<kPacked>::kThreads, 1)
+    weights_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapRows,
+                   const __grid_constant__ CUtensorMap mapKey, Args args) {
+    using C = Cfg<kPacked>;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ int s_plan[4], s_scratch[32];
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint8_t* base_ptr = smem_raw + (base - raw);
+    auto bar = [&](int i) { return base + C::kOffBars + 8u * i; };
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(base_ptr + C::kOffBars + 8 * (C::kBars + 1));
+    const uint64_t lim = args.wait_limit_ns;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int q_len = args.q_len;
+
+    if (threadIdx.x == 0) {
+        auto init = [&](int first, int n, int count) {
+            for (int i = 0; i < n; ++i) mbar_init(bar(first + i), count);
+        };
+        init(C::kQFull, kQChunks, 1);
+        init(C::kQEmpty, kQChunks, 1);
+        init(C::kChFull, C::kRing, kPacked ? 4 : 1);
+        init(C::kChEmpty, C::kRing, 1);
+        init(C::kSFull, 2, 1);
+        init(C::kSFree, 2, kSetWarps);
+        init(C::kRawFull, C::kRawStages, 1);
+        init(C::kRawEmpty, C::kRawStages, 4);
+        init(C::kKeyFull, 1, 1);
+        init(C::kKeyEmpty, 1, 1);
+        init(C::kDrain, 1, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+        prefetch_tensormap(&mapQ);
+        prefetch_tensormap(&mapRows);
+        if (kPacked) prefetch_tensormap(&mapKey);
+    }
+    if (warp == 1) {
+        tmem_alloc(bar(C::kBars), kTmemCols);
+        tmem_relinquish();
+    }
+    pdl_wait();
+    Pieces it;
+    plan_pieces(args, s_plan, s_scratch, it);  // its barriers also order the set-up above
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(base_ptr + C::kOffBars + 8 * C::kBars);
+    auto wait = [&](int i, int phase) { return warp_wait_shared(bar(i), phase & 1, lim); };
+
+    bool ok = true;
+    int seq = 0, T = 0, k0 = 0, k1 = 0;
+    int n_load = 0, n_pass = 0;  // loads and passes (query tokens of a block) begun
+    // Every role walks the same passes: tiles j0..j1-1 of a sequence against one of its query tokens.
+    auto walk = [&](auto&& pass) {
+        while (ok && it.next(seq, T, k0, k1)) {
+            const int step = q_len > 1 ? kBlock : k1 - k0;
+            for (int j0 = k0; j0 < k1 && ok; j0 += step) {
+                const int j1 = j0 + step < k1 ? j0 + step : k1;
+                for (int i = 0; i < q_len && ok; ++i, ++n_pass) ok = pass(j0, j1, i) && !*abort_flag;
+            }
+        }
+    };
+
+    if (warp == 0) {
+        // ======================================================== producer of rows
+        walk([&](int j0, int j1, int) {
+            if constexpr (kPacked) {
+#pragma unroll 1
+                for (int t = 2 * j0; t < 2 * j1; ++t, ++n_load) {
+                    const int st = n_load % C::kRawStages;
+                    if (!wait(C::kRawEmpty + st, n_load / C::kRawStages + 1)) return false;
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(bar(C::kRawFull + st), kRawBytes);
+                        tma_load_3d(base + C::kOffRaw + st * kRawBytes, &mapRows, bar(C::kRawFull + st), 0, t * kUnit, seq);
+                    }
+                    __syncwarp();
+                }
+            } else {
+#pragma unroll 1
+                for (int t = j0; t < j1; ++t)
+#pragma unroll 1
+                    for (int c = 0; c < kQChunks; ++c, ++n_load) {
+                        const int st = n_load % C::kRing;
+                        if (!wait(C::kChEmpty + st, n_load / C::kRing + 1)) return false;
+                        if (lane == 0) {
+                            mbar_arrive_expect_tx(bar(C::kChFull + st), kChunkBytes);
+                            tma_load_3d(base + C::kOffRing + st * kChunkBytes, &mapRows, bar(C::kChFull + st), 64 * c, t * kTile, seq);
+                        }
+                        __syncwarp();
+                    }
+            }
+            return true;
+        });
+    } else if (warp == 2) {
+        // ======================================================== producer of Q-hat, chunk by chunk behind the last products of the pass before
+        walk([&](int, int, int i) {
+#pragma unroll 1
+            for (int c = 0; c < kQChunks; ++c, ++n_load) {
+                if (!wait(C::kQEmpty + c, n_pass + 1)) return false;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(bar(C::kQFull + c), kChunkBytes);
+                    tma_load_3d(base + c * kChunkBytes, &mapQ, bar(C::kQFull + c), 64 * c, 0, seq * q_len + i);
+                }
+                __syncwarp();
+            }
+            return true;
+        });
+    } else if (kPacked && warp == 3) {
+        // ======================================================== producer of keys
+        walk([&](int j0, int j1, int) {
+#pragma unroll 1
+            for (int t = j0; t < j1; ++t, ++n_load) {
+                if (!wait(C::kKeyEmpty, n_load + 1)) return false;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(bar(C::kKeyFull), kChunkBytes);
+                    for (int r = 0; r < 2; ++r)
+                        tma_load_3d(base + C::kOffRing + r * kUnit * 128, &mapKey, bar(C::kKeyFull), 0, t * kTile + r * kUnit, seq);
+                }
+                __syncwarp();
+            }
+            return true;
+        });
+    } else if (warp == 1) {
+        // ======================================================== MMA issuer: S^T (128 rows x 128 heads) of tile after tile
+        constexpr uint32_t idS = idesc_bf16_f32(kTile, kHeads, false, false);
+        const uint64_t dQ = smem_desc(base, 16, 1024, kSw128);
+        const uint64_t dRing = smem_desc(base + C::kOffRing, 16, 1024, kSw128);
+        int used[2] = {0, 0};  // tiles each set has been given
+        int n = 0;             // ring chunks multiplied
+        walk([&](int j0, int j1, int) {
+#pragma unroll 1
+            for (int t = j0; t < j1; ++t) {
+                const int set = (t - j0) & 1;
+                const int uses = set ? used[1]++ : used[0]++;
+                if (!wait(C::kSFree + set, uses + 1)) return false;
+                const uint32_t dS = tmem + kTmemS + kHeads * set;
+#pragma unroll 1
+                for (int c = 0; c < kQChunks; ++c) {
+                    if (t == j0 && !wait(C::kQFull + c, n_pass)) return false;
+                    const bool key = kPacked && c == 8;  // the packed rows' keys
+                    const int st = n % C::kRing;
+                    if (!(key ? wait(C::kKeyFull, n_load) : wait(C::kChFull + st, n / C::kRing))) return false;
+                    tc_fence_after();
+                    if (elect_one()) {
+                        const uint64_t dB = dQ + ((c * kChunkBytes) >> 4);
+                        if (kPacked && !key) {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                mma_f16_ts(dS, tmem + kTmemRing + 32 * st + 8 * k, dB + ((32 * k) >> 4), idS, (c | k) ? 1u : 0u);
+                        } else {
+                            const uint64_t dA = key ? dRing : dRing + ((st * kChunkBytes) >> 4);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                mma_f16_ss(dS, dA + ((32 * k) >> 4), dB + ((32 * k) >> 4), idS, (c | k) ? 1u : 0u);
+                        }
+                        mma_commit(key ? bar(C::kKeyEmpty) : bar(C::kChEmpty + st));
+                        if (t == j1 - 1) mma_commit(bar(C::kQEmpty + c));
+                        if (c == kQChunks - 1) mma_commit(bar(C::kSFull + set));
+                    }
+                    __syncwarp();
+                    if (key) ++n_load;  // (tiles' keys multiplied)
+                    else ++n;
+                }
+            }
+            return true;
+        });
+        n_load = 0;
+    } else if (kPacked && warp >= 12) {
+        // ======================================================== unpacking warps: a row a lane, into the row's own TMEM lane
+        // Warps 12-15 take the even chunks, 16-19 the odd ones.
+        const int quarter = warp & 3, odd = warp >= 16 ? 1 : 0, hi = quarter >> 1;
+        const uint32_t lane_addr = (uint32_t)(quarter * 32) << 16;
+        int n = 0;  // tiles
+        walk([&](int j0, int j1, int) {
+#pragma unroll 1
+            for (int t = j0; t < j1; ++t, ++n) {
+                const int unit = 2 * n + hi, st = unit % C::kRawStages;
+                if (!wait(C::kRawFull + st, unit / C::kRawStages)) return false;
+                const uint32_t src = base + C::kOffRaw + st * kRawBytes + (32 * (quarter & 1) + lane) * kRawRow;
+                RawChunk r;
+                r.load(src, odd);
+#pragma unroll 1
+                for (int c = odd; c < 8; c += 2) {
+                    if (!wait(C::kChEmpty + c, n + 1)) return false;
+                    tc_fence_after();
+                    uint32_t v[32];
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+                        uint32_t x[8];
+                        unpack16<false>(r.w[2 * g], r.w[2 * g + 1], (r.scales >> (8 * g)) & 0xFFu, x);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) v[8 * g + j] = x[j];
+                    }
+                    tmem_st32(tmem + lane_addr + kTmemRing + 32 * c, v);
+                    if (c + 2 < 8) r.load(src, c + 2);
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(bar(C::kChFull + c));
+                        if (c >= 6) mbar_arrive(bar(C::kRawEmpty + st));
+                    }
+                }
+            }
+            return true;
+        });
+    } else if (warp >= 4 && warp < 12) {
+        // ======================================================== weights: lane = row of the tile; set 0 (warps 4-7) the even tiles of a block
+        const int set = warp >= 8 ? 1 : 0, quarter = warp & 3, row = quarter * 32 + lane;
+        float* nlse = reinterpret_cast<float*>(base_ptr + C::kOffLse) + (warp - 4) * kHeads;
+        float* sums = reinterpret_cast<float*>(base_ptr + C::kOffSums);
+        const uint32_t nl_addr = smem_u32(nlse);
+        const uint32_t s_addr = tmem + ((uint32_t)(quarter * 32) << 16) + kTmemS + kHeads * set;
+        int n = 0;  // tiles of this set
+        walk([&](int j0, int j1, int i) {
+            __syncwarp();
+            for (int h = lane; h < kHeads; h += 32) {
+                const float z = args.lse[((size_t)seq * q_len + i) * kHeads + h];
+                nlse[h] = z == -CUDART_INF_F ? -CUDART_INF_F : z * -1.4426950408889634f;
+            }
+            __syncwarp();
+#pragma unroll 1
+            for (int t = j0 + set; t < j1; t += 2, ++n) {
+                if (!wait(C::kSFull + set, n)) return false;
+                tc_fence_after();
+                float w0 = 0.f, w1 = 0.f;
+#pragma unroll 1
+                for (int h = 0; h < kHeads; h += 16) {
+                    uint32_t v[16];
+                    tmem_ld16(s_addr + h, v);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 16; j += 4) {
+                        uint32_t z[4];
+                        ld_shared_v4u(nl_addr + 4 * (h + j), z[0], z[1], z[2], z[3]);
+                        w0 += ex2(fmaf(__uint_as_float(v[j]), args.scale_log2, __uint_as_float(z[0])));
+                        w1 += ex2(fmaf(__uint_as_float(v[j + 1]), args.scale_log2, __uint_as_float(z[1])));
+                        w0 += ex2(fmaf(__uint_as_float(v[j + 2]), args.scale_log2, __uint_as_float(z[2])));
+                        w1 += ex2(fmaf(__uint_as_float(v[j + 3]), args.scale_log2, __uint_as_float(z[3])));
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(C::kSFree + set));
+                // query i sees rows 0..T-q_len+i; what a row past it holds reached only its own lane
+                const int r = t * kTile + row;
+                float w = r < T - q_len + 1 + i ? w0 + w1 : 0.f;
+                if (q_len > 1) {
+                    float* s = sums + (t - j0) * kTile + row;
+                    if (i > 0) w += *s;
+                    *s = w;
+                }
+                if (i == q_len - 1 && r < T) {
+                    const size_t at = (size_t)seq * args.stride_w + r;
+                    args.weights[at] = args.prev ? fmaf(args.decay, args.prev[at], w) : w;
+                }
+            }
+            return true;
+        });
+    }
+    if (!ok) *abort_flag = 1;
+
+    // ---- teardown: nothing this CTA issued may still run when it exits
+    __syncthreads();
+    pdl_trigger();
+    const bool aborted = *abort_flag != 0;
+    if (aborted && n_load > 0) {  // loads in flight (a producer warp's count; zero in the other roles)
+        const int first = warp == 0 ? (kPacked ? (int)C::kRawFull : (int)C::kChFull) : (warp == 2 ? (int)C::kQFull : (int)C::kKeyFull);
+        const int nst = warp == 0 ? (kPacked ? C::kRawStages : C::kRing) : (warp == 2 ? kQChunks : 1);
+        for (int x = n_load > nst ? n_load - nst : 0; x < n_load; ++x) mbar_wait(bar(first + x % nst), (x / nst) & 1, lim);
+    }
+    if (warp == 1 && lane == 0) mma_commit(bar(C::kDrain));
+    if (warp == 1) mbar_wait(bar(C::kDrain), 0, lim);
+    if (aborted && threadIdx.x == 0) atomicOr(args.status, MLA_STATUS_TIMEOUT);
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) tmem_dealloc(tmem, kTmemCols);
+}
+
+}  // namespace wt
+}  // namespace sm100
+}  // namespace mla
