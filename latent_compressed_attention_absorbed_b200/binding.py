@@ -132,16 +132,14 @@ def _need(t: torch.Tensor, name: str, dtype=None, ndim=None):
         raise ValueError(f"{name} must have {ndim} dims, got {tuple(t.shape)}")
 
 
-def _need_all(device, **tensors):
-    """Each (tensor, dtype, shape) is a contiguous CUDA tensor of that type and shape on ``device``; None passes."""
-    for name, (t, dtype, shape) in tensors.items():
-        if t is None:
-            continue
-        _need(t, name, dtype=dtype)
-        if tuple(t.shape) != tuple(shape):
-            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-        if t.device != device:
-            raise ValueError(f"{name} is on {t.device}, the other tensors on {device}")
+def _expect(t: Optional[torch.Tensor], name: str, dtype, shape: tuple, device):
+    """``t`` is a contiguous tensor of that type and shape on ``device``; None passes."""
+    if t is None or (t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous()):
+        return
+    _need(t, name, dtype=dtype)
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    raise ValueError(f"{name} is on {t.device}, the other tensors on {device}")
 
 
 def _need_weights(t, name, device, B):
@@ -168,6 +166,20 @@ class Library:
     def _check(self, rc: int):
         if rc != 0:
             raise MLAError(rc, self.lib.mla_last_error().decode())
+
+    def _call(self, fn, device: torch.device, stream, *args):
+        """fn(*args, stream) with ``device`` current, on ``stream`` (default: the device's current stream); raises on error."""
+        if stream is None:
+            raw = torch._C._cuda_getCurrentRawStream(device.index)
+        else:
+            raw = stream.cuda_stream
+        if torch._C._cuda_getDevice() == device.index:
+            rc = fn(*args, raw)
+        else:
+            with torch.cuda.device(device):
+                rc = fn(*args, raw)
+        if rc != 0:
+            self._check(rc)
 
     @staticmethod
     def dims(H, d_c, d_r, d_n, d_v, dtype, rope_base=10000.0, softmax_scale=0.0) -> Dims:
@@ -332,157 +344,155 @@ class Library:
             raise ValueError("these dims have no packed row (d_c must be a multiple of 16)")
         return n
 
-    def _any_cache(self, dims: Dims, cache: torch.Tensor, name: str = "cache", device=None):
-        """(descriptor, format) of a full-width or (uint8) packed cache."""
-        packed = cache.dtype == torch.uint8
-        if not packed and cache.dtype != self._dtype(dims):
+    def _any_cache(self, dims: Dims, cache: torch.Tensor, device, name: str = "cache", want: Optional[int] = None):
+        """(descriptor, format) of a full-width or (uint8) packed cache; ``want``: the one format the call takes."""
+        fmt = CACHE_PACKED if cache.dtype is torch.uint8 else CACHE_FULL
+        if fmt == CACHE_FULL and cache.dtype is not self._dtype(dims):
             raise TypeError(f"{name} must be {self._dtype(dims)} or torch.uint8 (packed), got {cache.dtype}")
+        if want is not None and fmt != want:
+            raise TypeError(f"the call takes a {('full-width', 'packed (torch.uint8)')[want]} cache, got {cache.dtype}")
         d = self.cache_desc(cache)
-        row = self.packed_row_bytes(dims) if packed else dims.d_c + dims.d_r
+        row = self.packed_row_bytes(dims) if fmt == CACHE_PACKED else dims.d_c + dims.d_r
         if cache.shape[2] < row:
             raise ValueError(f"{name} rows hold {cache.shape[2]} elements, {row} are needed")
-        if device is not None and cache.device != device:
+        if cache.device != device:
             raise ValueError(f"{name} is on {cache.device}, the other tensors on {device}")
-        return d, CACHE_PACKED if packed else CACHE_FULL
+        return d, fmt
 
-    def _packed_cache(self, dims: Dims, cache: torch.Tensor, device) -> Cache:
-        d, fmt = self._any_cache(dims, cache, device=device)
-        if fmt != CACHE_PACKED:
-            raise TypeError(f"a packed cache is torch.uint8, got {cache.dtype}")
-        return d
-
-    def _append(self, fn, dims, cd, c_kv, k_rope, pos, rows, stream):
-        dt = self._dtype(dims)
-        _need(c_kv, "c_kv", dtype=dt, ndim=3)
+    def _append(self, fn, want, dims, cache, c_kv, k_rope, pos, rows, stream):
+        dt, dev = self._dtype(dims), c_kv.device
+        cd, _ = self._any_cache(dims, cache, dev, want=want)
+        _need(c_kv, "c_kv", ndim=3)
         B, n_tok = c_kv.shape[0], c_kv.shape[1]
-        _need_all(c_kv.device, c_kv=(c_kv, dt, (B, n_tok, dims.d_c)), k_rope=(k_rope, dt, (B, n_tok, dims.d_r)),
-                  pos=(pos, torch.int32, (B,)), rows=(rows, torch.int32, (B,)))
-        with torch.cuda.device(c_kv.device):
-            self._check(fn(ctypes.byref(dims), _ptr(c_kv), _ptr(k_rope), _ptr(pos), _ptr(rows), B, n_tok,
-                           ctypes.byref(cd), _stream(stream)))
+        _expect(c_kv, "c_kv", dt, (B, n_tok, dims.d_c), dev)
+        _expect(k_rope, "k_rope", dt, (B, n_tok, dims.d_r), dev)
+        _expect(pos, "pos", torch.int32, (B,), dev)
+        _expect(rows, "rows", torch.int32, (B,), dev)
+        self._call(fn, dev, stream, dims, c_kv.data_ptr(), k_rope.data_ptr(), pos.data_ptr(),
+                   None if rows is None else rows.data_ptr(), B, n_tok, cd)
 
     def append_packed(self, dims: Dims, cache: torch.Tensor, c_kv: torch.Tensor, k_rope: torch.Tensor,
                       pos: torch.Tensor, rows: Optional[torch.Tensor] = None, stream=None):
         """Rows rows[b]+i (default pos[b]+i) of the packed cache <- [c_kv[b,i] in 4 bits || RoPE(k_rope[b,i], pos[b]+i)]."""
-        cd = self._packed_cache(dims, cache, c_kv.device)
-        self._append(self.lib.mla_append_packed, dims, cd, c_kv, k_rope, pos, rows, stream)
+        self._append(self.lib.mla_append_packed, CACHE_PACKED, dims, cache, c_kv, k_rope, pos, rows, stream)
 
     def append_rows(self, dims: Dims, cache: torch.Tensor, c_kv: torch.Tensor, k_rope: torch.Tensor, pos: torch.Tensor,
                     rows: torch.Tensor, stream=None):
         """append_cache with the row apart from the position (after rows have been evicted)."""
-        cd, fmt = self._any_cache(dims, cache, device=c_kv.device)
-        if fmt != CACHE_FULL:
-            raise TypeError("append_rows writes full-width rows: use append_packed for a packed cache")
-        self._append(self.lib.mla_append_rows, dims, cd, c_kv, k_rope, pos, rows, stream)
+        self._append(self.lib.mla_append_rows, CACHE_FULL, dims, cache, c_kv, k_rope, pos, rows, stream)
 
     def load_packed(self, dims: Dims, cache: torch.Tensor, rows: torch.Tensor, n_tok: int, out=None, stream=None):
         """Rows rows[b] .. rows[b]+n_tok-1 as full-width rows [B, n_tok, d_c + d_r]."""
+        dt, dev = self._dtype(dims), rows.device
+        cd, _ = self._any_cache(dims, cache, dev, want=CACHE_PACKED)
         _need(rows, "rows", dtype=torch.int32, ndim=1)
-        cd = self._packed_cache(dims, cache, rows.device)
-        shape = (rows.shape[0], n_tok, dims.d_c + dims.d_r)
+        B = rows.shape[0]
+        shape = (B, n_tok, dims.d_c + dims.d_r)
         if out is None:
-            out = torch.empty(shape, dtype=self._dtype(dims), device=rows.device)
-        _need_all(rows.device, out=(out, self._dtype(dims), shape))
-        with torch.cuda.device(rows.device):
-            self._check(self.lib.mla_load_packed(ctypes.byref(dims), ctypes.byref(cd), _ptr(rows), shape[0], n_tok,
-                                                 _ptr(out), _stream(stream)))
+            out = torch.empty(shape, dtype=dt, device=dev)
+        else:
+            _expect(out, "out", dt, shape, dev)
+        self._call(self.lib.mla_load_packed, dev, stream, dims, cd, rows.data_ptr(), B, n_tok, out.data_ptr())
         return out
 
     def packed_workspace_bytes(self, dims: Dims, B: int, q_len: int) -> int:
         return int(self.lib.mla_packed_workspace_bytes(ctypes.byref(dims), B, q_len))
 
-    def _workspace(self, workspace, nbytes, device):
+    @staticmethod
+    def _scratch(workspace, nbytes, device):
+        """The caller's workspace, or a new one of nbytes() bytes."""
         if workspace is None:
-            return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
+            with torch.cuda.device(device):  # (the size depends on the device)
+                n = nbytes()
+            return torch.empty(max(n, 16), dtype=torch.uint8, device=device)
         _need(workspace, "workspace", dtype=torch.uint8)
         if workspace.device != device:
             raise ValueError(f"workspace is on {workspace.device}, the other tensors on {device}")
         return workspace
 
+    def _attend(self, fn, want, size, dims, q_hat, cache, seqlens, out, lse, workspace, opts, stream):
+        dt, dev = self._dtype(dims), q_hat.device
+        cd, _ = self._any_cache(dims, cache, dev, want=want)
+        _need(q_hat, "q_hat", ndim=4)
+        B, q_len = q_hat.shape[0], q_hat.shape[1]
+        _expect(q_hat, "q_hat", dt, (B, q_len, dims.H, dims.d_c + dims.d_r), dev)
+        _expect(seqlens, "seqlens", torch.int32, (B,), dev)
+        _expect(lse, "lse", torch.float32, (B, q_len, dims.H), dev)
+        shape = (B, q_len, dims.H, dims.d_c)
+        if out is None:
+            out = torch.empty(shape, dtype=dt, device=dev)
+        else:
+            _expect(out, "out", dt, shape, dev)
+        ws = self._scratch(workspace, lambda: size(dims, B, q_len), dev)
+        self._call(fn, dev, stream, dims, q_hat.data_ptr(), cd, seqlens.data_ptr(), B, q_len, out.data_ptr(),
+                   None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.numel(), opts)
+        return out
+
     def attend_packed(self, dims: Dims, q_hat, cache, seqlens, out=None, lse=None, workspace=None,
                       opts: Optional[Opts] = None, stream=None):
         """attend_latent over a packed cache; ``lse`` (fp32 [B, q_len, H]) receives the log-sum-exps if given."""
-        dt, dev = self._dtype(dims), q_hat.device
-        _need(q_hat, "q_hat", dtype=dt, ndim=4)
-        B, q_len = q_hat.shape[0], q_hat.shape[1]
-        cd = self._packed_cache(dims, cache, dev)
-        if out is None:
-            out = torch.empty((B, q_len, dims.H, dims.d_c), dtype=dt, device=dev)
-        _need_all(dev, q_hat=(q_hat, dt, (B, q_len, dims.H, dims.d_c + dims.d_r)), seqlens=(seqlens, torch.int32, (B,)),
-                  out=(out, dt, (B, q_len, dims.H, dims.d_c)), lse=(lse, torch.float32, (B, q_len, dims.H)))
-        with torch.cuda.device(dev):
-            ws = self._workspace(workspace, 0 if workspace is not None else self.packed_workspace_bytes(dims, B, q_len), dev)
-            self._check(self.lib.mla_attend_packed(ctypes.byref(dims), _ptr(q_hat), ctypes.byref(cd), _ptr(seqlens), B,
-                                                   q_len, _ptr(out), _ptr(lse), _ptr(ws), ws.numel(),
-                                                   ctypes.byref(opts) if opts is not None else None, _stream(stream)))
-        return out
+        return self._attend(self.lib.mla_attend_packed, CACHE_PACKED, self.packed_workspace_bytes, dims, q_hat, cache,
+                            seqlens, out, lse, workspace, opts, stream)
 
     def decode_packed(self, dims: Dims, q_nope, q_rope, W_UK, W_UV, cache, seqlens, n_seen=None, out=None, q_hat=None,
                       lse=None, workspace=None, opts: Optional[Opts] = None, stream=None):
         """One decode step over a packed cache; returns out [B, q_len, H, d_v].  ``seqlens`` counts rows, ``n_seen``
         tokens (default: the same); ``q_hat`` and ``lse`` receive the folded queries and log-sum-exps if given."""
         dt, dev = self._dtype(dims), q_nope.device
-        _need(q_nope, "q_nope", dtype=dt, ndim=4)
+        cd, _ = self._any_cache(dims, cache, dev, want=CACHE_PACKED)
+        _need(q_nope, "q_nope", ndim=4)
         B, q_len = q_nope.shape[0], q_nope.shape[1]
-        cd = self._packed_cache(dims, cache, dev)
+        _expect(q_nope, "q_nope", dt, (B, q_len, dims.H, dims.d_n), dev)
+        _expect(q_rope, "q_rope", dt, (B, q_len, dims.H, dims.d_r), dev)
+        _expect(W_UK, "W_UK", dt, (dims.H, dims.d_n, dims.d_c), dev)
+        _expect(W_UV, "W_UV", dt, (dims.H, dims.d_v, dims.d_c), dev)
+        _expect(seqlens, "seqlens", torch.int32, (B,), dev)
+        _expect(n_seen, "n_seen", torch.int32, (B,), dev)
+        _expect(q_hat, "q_hat", dt, (B, q_len, dims.H, dims.d_c + dims.d_r), dev)
+        _expect(lse, "lse", torch.float32, (B, q_len, dims.H), dev)
+        shape = (B, q_len, dims.H, dims.d_v)
         if out is None:
-            out = torch.empty((B, q_len, dims.H, dims.d_v), dtype=dt, device=dev)
-        _need_all(dev, q_nope=(q_nope, dt, (B, q_len, dims.H, dims.d_n)), q_rope=(q_rope, dt, (B, q_len, dims.H, dims.d_r)),
-                  W_UK=(W_UK, dt, (dims.H, dims.d_n, dims.d_c)), W_UV=(W_UV, dt, (dims.H, dims.d_v, dims.d_c)),
-                  seqlens=(seqlens, torch.int32, (B,)), n_seen=(n_seen, torch.int32, (B,)),
-                  out=(out, dt, (B, q_len, dims.H, dims.d_v)), q_hat=(q_hat, dt, (B, q_len, dims.H, dims.d_c + dims.d_r)),
-                  lse=(lse, torch.float32, (B, q_len, dims.H)))
-        with torch.cuda.device(dev):
-            ws = self._workspace(workspace, 0 if workspace is not None else self.packed_workspace_bytes(dims, B, q_len), dev)
-            self._check(self.lib.mla_decode_packed(ctypes.byref(dims), _ptr(q_nope), _ptr(q_rope), _ptr(W_UK), _ptr(W_UV),
-                                                   ctypes.byref(cd), _ptr(seqlens), _ptr(n_seen), B, q_len, _ptr(out),
-                                                   _ptr(q_hat), _ptr(lse), _ptr(ws), ws.numel(),
-                                                   ctypes.byref(opts) if opts is not None else None, _stream(stream)))
+            out = torch.empty(shape, dtype=dt, device=dev)
+        else:
+            _expect(out, "out", dt, shape, dev)
+        ws = self._scratch(workspace, lambda: self.packed_workspace_bytes(dims, B, q_len), dev)
+        self._call(self.lib.mla_decode_packed, dev, stream, dims, q_nope.data_ptr(), q_rope.data_ptr(), W_UK.data_ptr(),
+                   W_UV.data_ptr(), cd, seqlens.data_ptr(), None if n_seen is None else n_seen.data_ptr(), B, q_len,
+                   out.data_ptr(), None if q_hat is None else q_hat.data_ptr(), None if lse is None else lse.data_ptr(),
+                   ws.data_ptr(), ws.numel(), opts)
         return out
 
     # ------------------------------------------------------------------ eviction by accumulated attention weight
     def attend_latent_lse(self, dims: Dims, q_hat, cache, seqlens, lse, out=None, workspace=None,
                           opts: Optional[Opts] = None, stream=None):
         """attend_latent that also writes the log-sum-exps to ``lse`` (fp32 [B, q_len, H])."""
-        dt, dev = self._dtype(dims), q_hat.device
-        _need(q_hat, "q_hat", dtype=dt, ndim=4)
-        B, q_len = q_hat.shape[0], q_hat.shape[1]
-        cd, fmt = self._any_cache(dims, cache, device=dev)
-        if fmt != CACHE_FULL:
-            raise TypeError("attend_latent_lse reads full-width rows: use attend_packed for a packed cache")
-        if out is None:
-            out = torch.empty((B, q_len, dims.H, dims.d_c), dtype=dt, device=dev)
-        _need_all(dev, q_hat=(q_hat, dt, (B, q_len, dims.H, dims.d_c + dims.d_r)), seqlens=(seqlens, torch.int32, (B,)),
-                  out=(out, dt, (B, q_len, dims.H, dims.d_c)), lse=(lse, torch.float32, (B, q_len, dims.H)))
-        with torch.cuda.device(dev):
-            ws = self._workspace(workspace, 0 if workspace is not None else self.workspace_bytes(dims, B, q_len), dev)
-            self._check(self.lib.mla_attend_latent_lse(ctypes.byref(dims), _ptr(q_hat), ctypes.byref(cd), _ptr(seqlens), B,
-                                                       q_len, _ptr(out), _ptr(lse), _ptr(ws), ws.numel(),
-                                                       ctypes.byref(opts) if opts is not None else None, _stream(stream)))
-        return out
+        if lse is None:
+            raise ValueError("lse must be given (attend_latent does without it)")
+        return self._attend(self.lib.mla_attend_latent_lse, CACHE_FULL, self.workspace_bytes, dims, q_hat, cache,
+                            seqlens, out, lse, workspace, opts, stream)
 
     def accumulate_weights(self, dims: Dims, q_hat, lse, cache, seqlens, weights, prev=None, decay: float = 1.0,
                            opts: Optional[Opts] = None, stream=None):
         """weights[b, t] = decay * prev[b, t] + the attention weight row t received in this step, summed over heads and
         queries (``prev``: None for zero, or ``weights`` itself); the cache is full-width or packed."""
-        dt, dev = self._dtype(dims), q_hat.device
-        _need(q_hat, "q_hat", dtype=dt, ndim=4)
-        B, q_len = q_hat.shape[0], q_hat.shape[1]
-        cd, fmt = self._any_cache(dims, cache, device=dev)
-        _need_all(dev, q_hat=(q_hat, dt, (B, q_len, dims.H, dims.d_c + dims.d_r)), lse=(lse, torch.float32, (B, q_len, dims.H)),
-                  seqlens=(seqlens, torch.int32, (B,)))
+        dev = q_hat.device
+        cd, fmt = self._any_cache(dims, cache, dev)
+        _need(q_hat, "q_hat", ndim=4)
+        B, q_len, rows = q_hat.shape[0], q_hat.shape[1], cache.shape[1]
+        _expect(q_hat, "q_hat", self._dtype(dims), (B, q_len, dims.H, dims.d_c + dims.d_r), dev)
+        _expect(lse, "lse", torch.float32, (B, q_len, dims.H), dev)
+        _expect(seqlens, "seqlens", torch.int32, (B,), dev)
         _need_weights(weights, "weights", dev, B)
-        if weights.shape[1] < cache.shape[1]:
-            raise ValueError(f"weights cover {weights.shape[1]} rows, the cache holds {cache.shape[1]}")
-        stride = weights.stride(0) if B > 1 else max(weights.stride(0), cache.shape[1])
-        if prev is not None:
+        if weights.shape[1] < rows:
+            raise ValueError(f"weights cover {weights.shape[1]} rows, the cache holds {rows}")
+        if prev is not None and prev is not weights:
             _need_weights(prev, "prev", dev, B)
             if prev.shape != weights.shape or (B > 1 and prev.stride(0) != weights.stride(0)):
                 raise ValueError("prev must have the shape and strides of weights")
-        with torch.cuda.device(dev):
-            self._check(self.lib.mla_accumulate_weights(ctypes.byref(dims), _ptr(q_hat), _ptr(lse), ctypes.byref(cd), fmt,
-                                                        _ptr(seqlens), B, q_len, decay, _ptr(prev), _ptr(weights), stride,
-                                                        ctypes.byref(opts) if opts is not None else None, _stream(stream)))
+        stride = weights.stride(0) if B > 1 else max(weights.stride(0), rows)
+        self._call(self.lib.mla_accumulate_weights, dev, stream, dims, q_hat.data_ptr(), lse.data_ptr(), cd, fmt,
+                   seqlens.data_ptr(), B, q_len, decay, None if prev is None else prev.data_ptr(), weights.data_ptr(),
+                   stride, opts)
         return weights
 
     def evict_workspace_bytes(self, dims: Dims, B: int, budget: int, packed: bool = False) -> int:
@@ -496,27 +506,28 @@ class Library:
         given; ``kept`` (int32 [B, budget]) receives the kept rows' indexes, -1 past their number."""
         _need(seqlens, "seqlens", dtype=torch.int32, ndim=1)
         dev, B = seqlens.device, seqlens.shape[0]
-        out = cache if out is None else out
-        out_weights = weights if out_weights is None else out_weights
-        out_seqlens = seqlens if out_seqlens is None else out_seqlens
-        cd, fmt = self._any_cache(dims, cache, device=dev)
-        od, out_fmt = self._any_cache(dims, out, "out", device=dev)
-        if fmt != out_fmt:
-            raise TypeError("out must be of the cache's kind")
+        cd, fmt = self._any_cache(dims, cache, dev)
+        od = cd if out is None else self._any_cache(dims, out, dev, "out", want=fmt)[0]
+        rows = cache.shape[1]
+        most = min(budget, rows)
         _need_weights(weights, "weights", dev, B)
-        _need_weights(out_weights, "out_weights", dev, B)
-        most = min(budget, cache.shape[1])
-        if weights.shape[1] < cache.shape[1] or out_weights.shape[1] < most:
-            raise ValueError(f"weights must cover {cache.shape[1]} rows and out_weights {most}")
-        _need_all(dev, out_seqlens=(out_seqlens, torch.int32, (B,)), kept=(kept, torch.int32, (B, budget)))
-        sw = weights.stride(0) if B > 1 else max(weights.stride(0), cache.shape[1])
-        so = sw if out_weights is weights else (out_weights.stride(0) if B > 1 else max(out_weights.stride(0), most))
-        with torch.cuda.device(dev):
-            n = 0 if workspace is not None else self.evict_workspace_bytes(dims, B, budget, fmt == CACHE_PACKED)
-            ws = self._workspace(workspace, n, dev)
-            self._check(self.lib.mla_evict(ctypes.byref(dims), ctypes.byref(cd), fmt, _ptr(weights), sw, _ptr(seqlens), B,
-                                           budget, n_sink, n_recent, ctypes.byref(od), _ptr(out_weights), so,
-                                           _ptr(out_seqlens), _ptr(kept), _ptr(ws), ws.numel(), _stream(stream)))
+        sw = weights.stride(0) if B > 1 else max(weights.stride(0), rows)
+        if out_weights is None or out_weights is weights:
+            out_weights, so = weights, sw
+        else:
+            _need_weights(out_weights, "out_weights", dev, B)
+            so = out_weights.stride(0) if B > 1 else max(out_weights.stride(0), most)
+        if weights.shape[1] < rows or out_weights.shape[1] < most:
+            raise ValueError(f"weights must cover {rows} rows and out_weights {most}")
+        if out_seqlens is None:
+            out_seqlens = seqlens
+        else:
+            _expect(out_seqlens, "out_seqlens", torch.int32, (B,), dev)
+        _expect(kept, "kept", torch.int32, (B, budget), dev)
+        ws = self._scratch(workspace, lambda: self.evict_workspace_bytes(dims, B, budget, fmt == CACHE_PACKED), dev)
+        self._call(self.lib.mla_evict, dev, stream, dims, cd, fmt, weights.data_ptr(), sw, seqlens.data_ptr(), B, budget,
+                   n_sink, n_recent, od, out_weights.data_ptr(), so, out_seqlens.data_ptr(),
+                   None if kept is None else kept.data_ptr(), ws.data_ptr(), ws.numel())
 
     def device_status(self, stream=None) -> int:
         """Synchronises the stream, returns and clears the device status bits."""

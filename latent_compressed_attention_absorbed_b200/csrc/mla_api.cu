@@ -84,8 +84,15 @@ int check_dims(const mla_dims_t* d, Problem* p) {
     p->scale = d->softmax_scale > 0.f ? d->softmax_scale : 1.0f / sqrtf((float)(d->d_n + d->d_r));
     p->B = 0;
     p->q_len = 1;
-    for (int k = 0; k < 64; ++k)
-        p->rope.inv_freq[k] = (k < d->d_r / 2) ? pow((double)d->rope_base, -2.0 * k / (double)d->d_r) : 0.0;
+    // 64 powers cost the host as much as a launch: kept until the base or width changes
+    static thread_local struct { float base = 0.f; int d_r = -1; RopeTable table; } t_rope;
+    if (t_rope.base != d->rope_base || t_rope.d_r != d->d_r) {
+        for (int k = 0; k < 64; ++k)
+            t_rope.table.inv_freq[k] = (k < d->d_r / 2) ? pow((double)d->rope_base, -2.0 * k / (double)d->d_r) : 0.0;
+        t_rope.base = d->rope_base;
+        t_rope.d_r = d->d_r;
+    }
+    p->rope = t_rope.table;
     return MLA_OK;
 }
 
