@@ -197,7 +197,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool softmax_warp = (warp >= 2 && warp <= 5) || (warp >= 12 && warp <= 15);
     const int kh = warp >= 12 ? 1 : 0;
     int n_load = 0;  // loads issued (a producer's lane 0), for the teardown
-    auto wait = [&](int i, int phase) { return warp_wait_shared(bar(i), phase & 1, lim); };
+    auto wait = [&](int i, int phase) { return warp_wait_fast<false>(bar(i), phase & 1, lim); };
+    auto wait_peer = [&](int i, int phase) { return warp_wait_fast<true>(bar(i), phase & 1, lim); };  // completed by the other CTA
 
     // The pieces of the group: sequence, tiles k0..k1-1, and whether they are all of it.
     SegIter it;
@@ -415,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 // p = 2^(s - m_used + 7)
                 const float mb = m_used == -CUDART_INF_F ? 0.f : kPShift - m_used;
-                if (ok && unit >= kSlots) ok = wait(kSlotFree + slot, unit / kSlots + 1);
+                if (ok && unit >= kSlots) ok = wait_peer(kSlotFree + slot, unit / kSlots + 1);
                 if (ok) {
                     const uint32_t stg = base + kOffStage + slot * kSlotBytes;
                     float rs0 = 0.f, rs1 = 0.f;
@@ -476,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
             for (; u < u1 && ok; ++u) {
                 const int slot = u % kSlots, st = u % kVStages;
-                if (!wait(kPFull + slot, u / kSlots) || !wait(kRescaled + slot, u / kSlots) || !wait(kVFull + st, u / kVStages) ||
+                if (!wait_peer(kPFull + slot, u / kSlots) || !wait(kRescaled + slot, u / kSlots) || !wait(kVFull + st, u / kVStages) ||
                     *abort_flag) {
                     ok = false;
                     break;
@@ -555,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
             for (; u < u1; ++u) {
                 const int slot = u % kSlots;
-                if (!wait(kPFull + slot, u / kSlots) || *abort_flag) { ok = false; break; }
+                if (!wait_peer(kPFull + slot, u / kSlots) || *abort_flag) { ok = false; break; }
                 const float* rowdat = slots + (slot * kSlotBytes + kSlotP) / 4 + 2 * m;
                 const float f = rowdat[0];
                 l_sum = ((u - u0) & 1) ? l_sum + rowdat[1] : rowdat[1];

@@ -118,15 +118,15 @@ __device__ __forceinline__ bool warp_wait_cluster(uint32_t bar, uint32_t parity,
     return __all_sync(0xffffffffu, mbar_wait_cluster(bar, parity, limit_ns));
 }
 
-// The whole-warp form as a function of its own: for kernels whose roles would
-// otherwise not fit the instruction cache (one copy of the spin loop serves
-// every wait).  Acquires at cluster scope, so it serves barriers completed by
-// either CTA of a pair.
-static __device__ __noinline__ bool warp_wait_shared(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
+// The whole-warp forms for kernels whose roles would otherwise not fit the
+// instruction cache: one inline test, for a barrier that is usually complete
+// by the time it is asked for, and one shared copy of the spin loop.
+template <bool kCluster>
+static __device__ __noinline__ bool warp_spin(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
     uint64_t t0 = 0;
     bool ok = true;
 #pragma unroll 1
-    for (uint32_t i = 1; !mbar_try_wait_cluster(bar, parity); ++i) {
+    for (uint32_t i = 1; !(kCluster ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)); ++i) {
         if ((i & 63) == 0) {
             const uint64_t now = global_timer_ns();
             if (t0 == 0) t0 = now;
@@ -137,6 +137,12 @@ static __device__ __noinline__ bool warp_wait_shared(uint32_t bar, uint32_t pari
         }
     }
     return __all_sync(0xffffffffu, ok);
+}
+template <bool kCluster>
+__device__ __forceinline__ bool warp_wait_fast(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
+    const bool ready = kCluster ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity);
+    if (__all_sync(0xffffffffu, ready)) return true;
+    return warp_spin<kCluster>(bar, parity, limit_ns);
 }
 
 // Spins for `ns` nanoseconds of the global timer (bounded by construction).

@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(Cfg<kPacked>::kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(base_ptr + C::kOffBars + 8 * C::kBars);
-    auto wait = [&](int i, int phase) { return warp_wait_shared(bar(i), phase & 1, lim); };
+    auto wait = [&](int i, int phase) { return warp_wait_fast<false>(bar(i), phase & 1, lim); };
 
     bool ok = true;
     int seq = 0, T = 0, k0 = 0, k1 = 0;
