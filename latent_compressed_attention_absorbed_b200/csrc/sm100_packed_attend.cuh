@@ -254,9 +254,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!wait(kSFree + sb, (g >> 1) + 1) || *abort_flag) { ok = false; break; }
                 const uint32_t dS = tmem + kTmemS + kTile * sb;
                 // eight chunks a tile: the ring of four returns to the same slots and phases every tile
-#pragma unroll 1
-                for (int c = 0; c < 8 && ok; ++c) {
-                    ok = wait(kChFull + c % kChunks, c / kChunks);
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    ok = ok && wait(kChFull + c % kChunks, c / kChunks);
                     tc_fence_after();
                     if (elect_one()) {
                         const uint64_t dB = dChunk + (((c % kChunks) * kChunkBytes) >> 4);
