@@ -356,7 +356,6 @@ cudaError_t sm100_attend_packed(const Problem& p, const void* q_hat, const Cache
     size_t off_part, off_lse;
     if (ws_bytes < attend_layout(p, clusters, &off_part, &off_lse)) return cudaErrorInvalidValue;
     char* ws = static_cast<char*>(workspace);
-    Plan* plan = reinterpret_cast<Plan*>(ws);
     CUtensorMap mRaw, mRope;
     const uint64_t stt = (uint64_t)cache.stride_t;
     const uint64_t sb = p.B > 1 ? (uint64_t)cache.stride_b : stt * (uint64_t)cache.T_max;
@@ -365,22 +364,23 @@ cudaError_t sm100_attend_packed(const Problem& p, const void* q_hat, const Cache
                         CU_TENSOR_MAP_SWIZZLE_NONE) ||
         !make_map(&mRope, rows + kPackRope, kRope, cache.T_max, p.B, stt, sb, kRope, pk::kUnit, 1, CU_TENSOR_MAP_SWIZZLE_128B))
         return cudaErrorInvalidValue;
-    mla_plan_kernel<pk::kTile><<<1, 32, 0, st>>>(seqlens, p.B, p.q_len, cache.T_max, clusters,
-                                                 opts && opts->overhead_tiles >= 0 ? opts->overhead_tiles : 1,
-                                                 opts && opts->min_tiles > 0 ? opts->min_tiles : 1, plan, status,
-                                                 (__nv_bfloat16*)o_lat, lse);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
+    cudaError_t e;
     e = set_smem(pk::packed_attend_kernel, pk::kSmem, g_smem_packed);
     if (e != cudaSuccess) return e;
     pk::Args a;
-    a.plan = plan;
     a.seqlens = seqlens;
+    a.B = p.B;
     a.q_len = p.q_len;
+    a.T_max = cache.T_max;
+    a.ovh = opts && opts->overhead_tiles >= 0 ? opts->overhead_tiles : 1;
+    a.min_units = opts && opts->min_tiles > 0 ? opts->min_tiles : 1;
     a.scale_log2 = p.scale * 1.4426950408889634f;
     a.q_hat = (const __nv_bfloat16*)q_hat;
     a.o_lat = (__nv_bfloat16*)o_lat;
     a.o_lat_v8 = (reinterpret_cast<uintptr_t>(o_lat) & 31u) == 0;
+    const int groups = clusters / p.q_len;
+    a.cuts = reinterpret_cast<int4*>(ws);  // (in the plan's place)
+    a.cuts_by_seq = p.B < groups;
     a.part_o = reinterpret_cast<float*>(ws + off_part);
     a.part_lse = reinterpret_cast<float*>(ws + off_lse);
     a.lse = lse;
@@ -388,10 +388,18 @@ cudaError_t sm100_attend_packed(const Problem& p, const void* q_hat, const Cache
     a.wait_limit_ns = (opts && opts->wait_limit_ns > 0) ? (uint64_t)opts->wait_limit_ns : MLA_WAIT_LIMIT_NS;
     e = launch_pdl(pk::packed_attend_kernel, dim3(clusters * 2), dim3(pk::kThreads), pk::kSmem, st, 2, mRaw, mRope, a);
     if (e != cudaSuccess) return e;
-    const int units = p.B * p.q_len;
-    const int max_split = units < clusters ? units : clusters;
-    return launch_pdl(mla_combine_kernel, dim3(max_split * (kHeads / 8)), dim3(256), 0, st, 1, (const Plan*)plan,
-                      (const float*)a.part_o, (const float*)a.part_lse, (__nv_bfloat16*)o_lat, lse);
+    if (groups < 2) return cudaSuccess;  // nothing is cut
+    pk::MergeArgs m;
+    m.cuts = a.cuts;
+    m.q_len = p.q_len;
+    m.part_o = a.part_o;
+    m.part_lse = a.part_lse;
+    m.o_lat = a.o_lat;
+    m.lse = lse;
+    const int tokens = (a.cuts_by_seq ? p.B : groups - 1) * p.q_len;
+    if (tokens <= 8)
+        return launch_pdl(pk::packed_merge_kernel<1, 16>, dim3(tokens * kHeads), dim3(512), 0, st, 1, m);
+    return launch_pdl(pk::packed_merge_kernel<8, 2>, dim3(tokens * (kHeads / 8)), dim3(512), 0, st, 1, m);
 }
 
 template <bool kPacked>

@@ -29,16 +29,18 @@
 //     sequence's end need no clearing: their scores are replaced by -infinity
 //     (a NaN key only reaches its own score), and 0 times a finite number is 0.
 //
-// Roles (736 threads; warp w reaches TMEM lanes 32*(w%4)..+31):
-//   scorer:      warp 0 TMA producer; 1 TMEM owner and S issuer; 2-5 and 12-15 softmax (two per TMEM quarter, 64 keys
-//                each); 6-9 Q-hat loaders; 10, 11, 16-21 unpack; 22 producer of keys
-//   accumulator: warp 0 TMA producer; 1 TMEM owner and O issuer; 2-5 and 12-15 rescale / epilogue (two per quarter, 256
-//                columns each); 6-9 and 16-19 unpack; 10 returns consumed P slots
+// Roles (640 threads; warp w reaches TMEM lanes 32*(w%4)..+31):
+//   scorer:      warp 0 producer of packed rows; 1 TMEM owner and S issuer; 2-5 and 12-15 softmax (two per TMEM quarter,
+//                64 keys each); 10, 11, 16, 17 unpack even chunks; 6-9 load Q-hat once a piece and unpack odd chunks;
+//                18 producer of keys
+//   accumulator: warp 0 producer of packed rows; 1 TMEM owner and O issuer; 2-5 and 12-15 rescale / epilogue (two per
+//                quarter, 256 columns each); 6-9 and 16-19 unpack; 10 returns consumed P slots; 11 notes the cuts
 // Every wait is bounded and its expiry ends the kernel in order, as in
 // sm100_attend.cuh.
 #pragma once
 
 #include "sm100_attend.cuh"
+#include "sm100_pieces.cuh"
 #include "sm100_unpack.cuh"
 
 namespace mla {
@@ -47,7 +49,7 @@ namespace pk {
 
 constexpr int kTile = 128;  // keys of a score tile
 constexpr int kUnit = 64;   // keys of a P slot and of an accumulator stage
-constexpr int kThreads = 736;
+constexpr int kThreads = 640;
 
 constexpr int kRawRow = kPackNib + kPackScale;    // codes and scales of a row as they lie in memory: 288 bytes
 constexpr int kRawBox = kUnit * kRawRow;          // 64 keys, 18 KB
@@ -113,9 +115,9 @@ enum {
 static_assert(8 * (kBars + 2) <= 512, "barrier block too small");
 
 struct Args {
-    const Plan* plan;
     const int32_t* seqlens;
-    int q_len;
+    int B, q_len, T_max;
+    int ovh, min_units;  // of the split, in tiles
     float scale_log2;
     const __nv_bfloat16* q_hat;  // [B][q_len][128][576]
     __nv_bfloat16* o_lat;        // [B][q_len][128][512]
@@ -123,6 +125,8 @@ struct Args {
     float* part_o;
     float* part_lse;
     float* lse;                  // [B][q_len][128] or NULL
+    int4* cuts;                  // what the merge has to do, by sequence (cuts_by_seq) or by group: {sequence or -1, first, last group}
+    int cuts_by_seq;
     int* status;
     uint64_t wait_limit_ns;
 };
@@ -132,6 +136,8 @@ struct Args {
 __global__ void __launch_bounds__(kThreads, 1)
     packed_attend_kernel(const __grid_constant__ CUtensorMap mapRaw, const __grid_constant__ CUtensorMap mapRope, Args args) {
     extern __shared__ uint8_t smem_raw[];
+    __shared__ int s_scratch[64];
+    __shared__ PieceShare s_share;
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
     uint8_t* base_ptr = smem_raw + (base - raw);
@@ -189,7 +195,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(base_ptr + kOffBars + 8 * kBars);
     pdl_wait();
     if (threadIdx.x == 0) pdl_trigger();
-    const bool active = grp < args.plan->groups;
+    // The clusters form groups of q_len, one cluster a query token; groups past the last whole one idle.
+    const int groups = (int)(gridDim.x / 2) / q_len;
+    const Batch batch = {args.seqlens, args.B, q_len, args.T_max, kTile, args.ovh};
+    plan_share(batch, groups, grp, args.min_units, true, s_scratch, &s_share);
+    const bool active = grp < groups;
+    // Sequences with an invalid length: zeros, and -infinity for the log-sum-exps.
+    for (int b = blockIdx.x; b < args.B; b += gridDim.x) {
+        if (batch.valid(batch.len(b))) continue;
+        if (threadIdx.x == 0) {
+            atomicOr(args.status, MLA_STATUS_BAD_SEQLEN);
+            if (args.cuts_by_seq) args.cuts[b] = make_int4(-1, 0, 0, 0);
+        }
+        uint4* o = reinterpret_cast<uint4*>(args.o_lat + (size_t)b * q_len * kHeads * kLat);
+        for (int i = threadIdx.x; i < q_len * kHeads * kLat / 8; i += kThreads) o[i] = make_uint4(0, 0, 0, 0);
+        for (int i = threadIdx.x; args.lse && i < q_len * kHeads; i += kThreads)
+            args.lse[(size_t)b * q_len * kHeads + i] = -CUDART_INF_F;
+    }
 
     const int quarter = warp & 3;
     const int m = quarter * 32 + lane;
@@ -201,17 +223,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto wait_peer = [&](int i, int phase) { return warp_wait_fast<true>(bar(i), phase & 1, lim); };  // completed by the other CTA
 
     // The pieces of the group: sequence, tiles k0..k1-1, and whether they are all of it.
-    SegIter it;
-    int seq = 0, k0 = 0, k1 = 0;
+    Pieces it(&s_share);
+    int seq = 0, T = 0, k0 = 0, k1 = 0;
     bool whole = false, ok = true;
-    if (active) it.init(args.plan, grp);
     if (!active) {
         // idle cluster (the cluster count is not a multiple of q_len)
     } else if (warp == 0) {
         // ======================================================== producer of packed rows (both CTAs), 64 rows a copy
         const int per = rank == 0 ? 2 : 1;  // copies of a stage
         const int full = rank == 0 ? (int)kRawFull : (int)kARawFull, empty = rank == 0 ? (int)kRawEmpty : (int)kARawEmpty;
-        while (ok && it.next(seq, k0, k1, whole)) {
+        while (ok && it.next(seq, T, k0, k1, whole)) {
 #pragma unroll 1
             for (int t = 2 * k0; t < 2 * k1; t += per, ++n_load) {
                 const int st = n_load % kRawStages;
@@ -225,9 +246,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
             }
         }
-    } else if (rank == 0 && warp == 22) {
+    } else if (rank == 0 && warp == 18) {
         // ======================================================== scorer: producer of RoPE keys
-        while (ok && it.next(seq, k0, k1, whole)) {
+        while (ok && it.next(seq, T, k0, k1, whole)) {
 #pragma unroll 1
             for (int t = k0; t < k1; ++t, ++n_load) {
                 if (!wait(kRopeEmpty, n_load + 1) || *abort_flag) { ok = false; break; }
@@ -246,7 +267,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t dRope = smem_desc(base + kOffRope, 16, 1024, kSw128);
         const uint64_t dQ = smem_desc(base + kOffQ, 16, 1024, kSw128);
         int g = 0;
-        for (int seg = 0; ok && it.next(seq, k0, k1, whole); ++seg) {
+        for (int seg = 0; ok && it.next(seq, T, k0, k1, whole); ++seg) {
             ok = wait(kQFull, seg);
 #pragma unroll 1
             for (int t = k0; t < k1 && ok; ++t, ++g) {
@@ -279,13 +300,60 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
             }
         }
-    } else if (rank == 0 && (warp == 10 || warp == 11 || warp >= 16)) {
+    } else if (rank == 0 && ((warp >= 6 && warp <= 11) || warp == 16 || warp == 17)) {
         // ======================================================== scorer: unpacking warps, a row of the tile a lane
-        // Two sets of four warps take the even and the odd chunks.
-        const int w8 = warp < 12 ? warp - 10 : warp - 14;
-        const int odd = w8 >> 2, row = 32 * (w8 & 3) + lane;
+        // Two sets of four warps take the even (10, 11, 16, 17) and the odd chunks
+        // (6-9).  The second set first loads a piece's Q-hat: row m's 512 latent
+        // values -> TMEM columns 0..255, read coalesced and transposed through the
+        // RoPE part's own buffer, where the last block, the RoPE part, stays as
+        // the shared-memory operand.
+        const bool loader = warp <= 9;
+        const int odd = loader ? 1 : 0;
+        const int row = 32 * (loader ? quarter : (warp < 12 ? warp - 10 : warp - 14)) + lane;
         int g = 0;
-        while (ok && it.next(seq, k0, k1, whole)) {
+        for (int seg = 0; ok && it.next(seq, T, k0, k1, whole); ++seg) {
+            if (loader) {
+                // the last S of the previous piece has read Q-hat
+                if (!wait(kQRead, seg + 1) || *abort_flag) { ok = false; break; }
+                tc_fence_after();
+                const uint32_t qbuf = base + kOffQ + quarter * 32 * 128;
+                const int rr = lane >> 3, pc = lane & 7;
+                const int u = seq * q_len + qi;
+                const uint4* src = reinterpret_cast<const uint4*>(args.q_hat + ((size_t)u * kHeads + quarter * 32 + rr) * kRow) + pc;
+                uint4 cur[8], nxt[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) cur[j] = __ldg(src + (size_t)(4 * j) * (kRow / 8));
+#pragma unroll 1
+                for (int c = 0; c < 9; ++c) {
+                    if (c + 1 < 9) {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) nxt[j] = __ldg(src + (size_t)(4 * j) * (kRow / 8) + 8 * (c + 1));
+                    }
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const int r = 4 * j + rr;
+                        st_shared_v4(qbuf + sw128(r, pc), cur[j].x, cur[j].y, cur[j].z, cur[j].w);
+                    }
+                    __syncwarp();
+                    if (c == 8) break;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t v[16];
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            ld_shared_v4u(qbuf + sw128(lane, 4 * h + q), v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+                        tmem_st16(tmem + lane_addr + kTmemQ + 32 * c + 16 * h, v);
+                    }
+                    __syncwarp();
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) cur[j] = nxt[j];
+                }
+                tmem_wait_st();
+                fence_proxy_async_smem();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(kQFull));
+            }
 #pragma unroll 1
             for (int t = k0; t < k1 && ok; ++t, ++g) {
                 const int st = g % kRawStages;
@@ -308,53 +376,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
         }
-    } else if (rank == 0 && warp >= 6 && warp <= 9) {
-        // ======================================================== scorer: Q-hat loaders (once per piece)
-        // Row m's 512 latent values -> TMEM columns 0..255, read coalesced and
-        // transposed through the RoPE part's own buffer, where the last block,
-        // the RoPE part, stays as the shared-memory operand.
-        const uint32_t qbuf = base + kOffQ + quarter * 32 * 128;
-        const int rr = lane >> 3, pc = lane & 7;
-        for (int seg = 0; ok && it.next(seq, k0, k1, whole); ++seg) {
-            // the last S of the previous piece has read Q-hat
-            if (!wait(kQRead, seg + 1) || *abort_flag) { ok = false; break; }
-            tc_fence_after();
-            const int u = seq * q_len + qi;
-            const uint4* src = reinterpret_cast<const uint4*>(args.q_hat + ((size_t)u * kHeads + quarter * 32) * kRow);
-            uint4 cur[8], nxt[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) cur[j] = __ldg(src + (size_t)(4 * j + rr) * (kRow / 8) + pc);
-#pragma unroll 1
-            for (int c = 0; c < 9; ++c) {
-                if (c + 1 < 9) {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) nxt[j] = __ldg(src + (size_t)(4 * j + rr) * (kRow / 8) + 8 * (c + 1) + pc);
-                }
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int row = 4 * j + rr;
-                    st_shared_v4(qbuf + sw128(row, pc), cur[j].x, cur[j].y, cur[j].z, cur[j].w);
-                }
-                __syncwarp();
-                if (c == 8) break;
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t v[16];
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        ld_shared_v4u(qbuf + sw128(lane, 4 * h + q), v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
-                    tmem_st16(tmem + lane_addr + kTmemQ + 32 * c + 16 * h, v);
-                }
-                __syncwarp();
-#pragma unroll
-                for (int j = 0; j < 8; ++j) cur[j] = nxt[j];
-            }
-            tmem_wait_st();
-            fence_proxy_async_smem();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(kQFull));
-        }
     } else if (rank == 0 && softmax_warp) {
         // ======================================================== scorer: softmax warps
         // Half kh of a quarter's pair takes keys 64kh..64kh+63 of each score
@@ -368,10 +389,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float sl2 = args.scale_log2;
         int g = 0;
         bool run = true;  // the pair's common decision
-        while (run && it.next(seq, k0, k1, whole)) {
+        while (run && it.next(seq, T, k0, k1, whole)) {
             float m_used = -CUDART_INF_F, l_part = 0.f;
             // query token qi of sequence b sees keys 0..T_b-q_len+qi
-            const int n_keys = args.seqlens[seq] - q_len + 1 + qi;
+            const int n_keys = T - q_len + 1 + qi;
 #pragma unroll 1
             for (int t = k0; t < k1; ++t, ++g) {
                 const int sb = g & 1, unit = 2 * g + kh, slot = unit % kSlots;
@@ -471,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t dP = smem_desc(base + kOffSlots, 16, 1024, kSw128);
         const uint64_t dV = smem_desc(base + kOffV, kVChunk, 1024, kSw128);
         int u = 0;
-        for (int seg = 0; ok && it.next(seq, k0, k1, whole); ++seg) {
+        for (int seg = 0; ok && it.next(seq, T, k0, k1, whole); ++seg) {
             ok = wait(kOFree, seg + 1);  // the previous piece's O has been read
             const int u0 = u, u1 = u + 2 * (k1 - k0);
 #pragma unroll 1
@@ -505,7 +526,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int w8 = warp < 10 ? warp - 6 : warp - 12, part = w8 >> 1;
         const int row = 32 * (w8 & 1) + lane;
         int u = 0;
-        while (ok && it.next(seq, k0, k1, whole)) {
+        while (ok && it.next(seq, T, k0, k1, whole)) {
             const int u1 = u + 2 * (k1 - k0);
 #pragma unroll 1
             for (; u < u1; ++u) {
@@ -530,9 +551,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (rank == 1 && warp == 10) {
         // ======================================================== accumulator: slot forwarder
         // Arms each P slot for the unit to come, then tells the scorer that it is free.
-        SegIter all = it;
+        Pieces all = it;
         int n_units = 0;
-        while (all.next(seq, k0, k1, whole)) n_units += 2 * (k1 - k0);
+        while (all.next(seq, T, k0, k1, whole)) n_units += 2 * (k1 - k0);
         const uint32_t slotfree_peer = mapa(bar(kSlotFree), peer);
         if (lane == 0)
             for (int s = 0; s < kSlots && s < n_units; ++s) mbar_arrive_expect_tx(bar(kPFull + s), kSlotBytes);
@@ -545,12 +566,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_arrive_remote_relaxed(slotfree_peer + 8 * slot);
             }
         }
+    } else if (rank == 1 && warp == 11) {
+        // ======================================================== accumulator: what the merge has to know
+        if (qi == 0) {
+            int4 last = make_int4(-1, 0, 0, 0);
+            while (it.next(seq, T, k0, k1, whole)) {
+                if (k0 > 0) continue;
+                last = make_int4(whole ? -1 : seq, grp, (it.pre - 1) / s_share.L, 0);
+                if (args.cuts_by_seq && lane == 0) args.cuts[seq] = last;
+            }
+            if (!args.cuts_by_seq && lane == 0) args.cuts[grp] = last;
+        }
     } else if (rank == 1 && softmax_warp) {
         // ======================================================== accumulator: rescale / epilogue warps
         const float* slots = reinterpret_cast<const float*>(base_ptr + kOffSlots);
         const uint32_t o_addr = tmem + lane_addr + 256 * kh;
         int u = 0;
-        for (int seg = 0; ok && it.next(seq, k0, k1, whole); ++seg) {
+        for (int seg = 0; ok && it.next(seq, T, k0, k1, whole); ++seg) {
             float l_sum = 0.f;
             const int u0 = u, u1 = u + 2 * (k1 - k0);
 #pragma unroll 1
@@ -639,6 +671,78 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool peer_aborted = ld_shared_cluster_u32(mapa(abort_addr, peer)) != 0;
     cluster_sync();
     if (aborted || peer_aborted) spin_ns(20000);
+}
+
+// The merge of sequences that were cut: o = sum_p 2^(lse_p - m) o_p / sum_p 2^(lse_p - m).
+// The group that holds a cut sequence's first part has left its number and the
+// last group of it.  A CTA merges kHeadsPer heads of one query token, kWays
+// warps a head: each takes every kWays-th piece, a whole row of 512 columns at
+// a time (four independent loads a lane), and the warps' states meet in shared
+// memory.  16 warps for one head where there are few tokens (32 pieces of one
+// sequence in two rounds; eight heads a CTA and one warp a head: 18 us), two
+// for each of eight heads where there are many, most of them in few pieces.
+struct MergeArgs {
+    const int4* cuts;
+    int q_len;
+    const float* part_o;
+    const float* part_lse;
+    __nv_bfloat16* o_lat;
+    float* lse;
+};
+
+template <int kHeadsPer, int kWays>
+__global__ void __launch_bounds__(kHeadsPer * kWays * 32) packed_merge_kernel(MergeArgs a) {
+    __shared__ float s_m[kHeadsPer * kWays], s_w[kHeadsPer * kWays];
+    __shared__ float4 s_acc[kHeadsPer][kWays - 1][kLat / 4];
+    const int blk = blockIdx.x / (kHeads / kHeadsPer);
+    const int qi = blk % a.q_len;
+    pdl_wait();
+    pdl_trigger();
+    const int4 cut = a.cuts[blk / a.q_len];
+    if (cut.x < 0) return;
+    const int p_lo = cut.y, p_hi = cut.z;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int hh = warp / kWays, way = warp % kWays;
+    const int h = (blockIdx.x % (kHeads / kHeadsPer)) * kHeadsPer + hh;
+    const size_t tok = (size_t)cut.x * a.q_len + qi;  // piece p is in slot p q_len + tok
+    MergeState st;
+    st.clear();
+#pragma unroll 1
+    for (int p = p_lo + way; p <= p_hi; p += kWays) {
+        const size_t slot = tok + (size_t)p * a.q_len;
+        // columns 4q..4q+3, q = lane + 32 j: octet q / 2, half q % 2
+        const float4* src = reinterpret_cast<const float4*>(a.part_o) + (slot * (kLat / 8) * kHeads + h) * 2;
+        float4 v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int q = lane + 32 * j;
+            v[j] = __ldg(src + (size_t)(q / 2) * kHeads * 2 + (q % 2));
+        }
+        const float z = __ldg(a.part_lse + slot * kHeads + h);
+        st.fold(z, z == -CUDART_INF_F ? 0.f : 1.f, v);
+    }
+    if (way > 0) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s_acc[hh][way - 1][lane + 32 * j] = st.acc[j];
+        if (lane == 0) {
+            s_m[warp] = st.m;
+            s_w[warp] = st.wsum;
+        }
+    }
+    __syncthreads();
+    if (way > 0) return;
+#pragma unroll 1
+    for (int w = 1; w < kWays; ++w) {
+        float4 v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = s_acc[hh][w - 1][lane + 32 * j];
+        st.fold(s_m[warp + w], s_w[warp + w], v);
+    }
+    if (a.lse && lane == 0) a.lse[tok * kHeads + h] = lse_natural(st.m, st.wsum);
+    st.normalise();
+    uint2* dst = reinterpret_cast<uint2*>(a.o_lat + (tok * kHeads + h) * kLat) + lane;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) dst[32 * j] = make_uint2(pack_bf16(st.acc[j].x, st.acc[j].y), pack_bf16(st.acc[j].z, st.acc[j].w));
 }
 
 }  // namespace pk

@@ -30,6 +30,7 @@
 #include <math_constants.h>
 
 #include "sm100_attend.cuh"
+#include "sm100_pieces.cuh"
 #include "sm100_unpack.cuh"
 
 namespace mla {
@@ -91,87 +92,6 @@ struct Args {
     uint64_t wait_limit_ns;
 };
 
-// The tile ranges of a CTA: every sequence costs its tiles and one more (its
-// Q-hat); the CTA's share is units lo..hi-1 of that list.
-struct Pieces {
-    const int32_t* seqlens;
-    int B, q_len, T_max, lo, hi, pre, b;
-    static __device__ __forceinline__ int cost(int T, int q_len, int T_max) {
-        return T < q_len || T > T_max ? 0 : (T + kTile - 1) / kTile + 1;
-    }
-    __device__ bool next(int& seq, int& T, int& k0, int& k1) {
-        while (b < B && pre < hi) {
-            const int len = seqlens[b], c = cost(len, q_len, T_max);
-            int s = lo - pre - 1, e = hi - pre - 1;
-            s = s < 0 ? 0 : s;
-            e = e > c - 1 ? c - 1 : e;
-            const int cur = b++;
-            pre += c;
-            if (e > s) {
-                seq = cur;
-                T = len;
-                k0 = s;
-                k1 = e;
-                return true;
-            }
-        }
-        return false;
-    }
-};
-
-// Share of every CTA and the sequence this one starts in (all threads; two
-// block barriers).  plan: {units a CTA, first sequence, its first unit}.
-__device__ __forceinline__ void plan_pieces(const Args& a, int* plan, int* scratch, Pieces& p) {
-    const int n = blockDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int per = (a.B + n - 1) / n;
-    const int b0 = tid * per;
-    int sum = 0;
-    bool bad = false;
-    for (int b = b0; b < b0 + per && b < a.B; ++b) {
-        const int c = Pieces::cost(a.seqlens[b], a.q_len, a.T_max);
-        bad |= c == 0;
-        sum += c;
-    }
-    if (bad && blockIdx.x == 0) atomicOr(a.status, MLA_STATUS_BAD_SEQLEN);
-    int inc = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += y;
-    }
-    if (lane == 31) scratch[warp] = inc;
-    if (tid == 0) plan[1] = a.B;
-    __syncthreads();
-    int before = 0, total = 0;
-    for (int w = 0; w < n / 32; ++w) {
-        const int s = scratch[w];
-        if (w < warp) before += s;
-        total += s;
-    }
-    const int share = (total + gridDim.x - 1) / gridDim.x;
-    const int lo = blockIdx.x * share;
-    int pre = before + inc - sum;
-    if (lo >= pre && lo < pre + sum) {
-        int b = b0;
-        for (;; ++b) {
-            const int c = Pieces::cost(a.seqlens[b], a.q_len, a.T_max);
-            if (lo < pre + c) break;
-            pre += c;
-        }
-        plan[1] = b;
-        plan[2] = pre;
-    }
-    __syncthreads();
-    p.seqlens = a.seqlens;
-    p.B = a.B;
-    p.q_len = a.q_len;
-    p.T_max = a.T_max;
-    p.lo = lo;
-    p.hi = lo + share;
-    p.b = plan[1];
-    p.pre = p.b < a.B ? plan[2] : 0;
-}
-
 // mapQ: Q-hat [tokens][128 heads][576], box 64 x 128 x 1, SW128.
 // full width: mapRows [B][T_max][576], box 64 x 128 rows, SW128 (mapKey unused);
 // packed: mapRows the codes and scales [B][T_max][144 words], box 144 x 64 rows; mapKey the keys, box 64 x 64 rows, SW128.
@@ -181,7 +101,8 @@ __global__ void __launch_bounds__(Cfg<kPacked>::kThreads, 1)
                    const __grid_constant__ CUtensorMap mapKey, Args args) {
     using C = Cfg<kPacked>;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ int s_plan[4], s_scratch[32];
+    __shared__ int s_scratch[64];
+    __shared__ PieceShare s_share;
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
     uint8_t* base_ptr = smem_raw + (base - raw);
@@ -217,20 +138,23 @@ __global__ void __launch_bounds__(Cfg<kPacked>::kThreads, 1)
         tmem_relinquish();
     }
     pdl_wait();
-    Pieces it;
-    plan_pieces(args, s_plan, s_scratch, it);  // its barriers also order the set-up above
+    const Batch batch = {args.seqlens, args.B, q_len, args.T_max, kTile, 1};
+    plan_share(batch, gridDim.x, blockIdx.x, 1, false, s_scratch, &s_share);
+    Pieces it(&s_share);
+    for (int b = blockIdx.x + gridDim.x * threadIdx.x; b < args.B; b += gridDim.x * blockDim.x)
+        if (!batch.valid(batch.len(b))) atomicOr(args.status, MLA_STATUS_BAD_SEQLEN);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(base_ptr + C::kOffBars + 8 * C::kBars);
     auto wait = [&](int i, int phase) { return warp_wait_fast<false>(bar(i), phase & 1, lim); };
 
-    bool ok = true;
+    bool ok = true, whole = false;
     int seq = 0, T = 0, k0 = 0, k1 = 0;
     int n_load = 0, n_pass = 0;  // loads and passes (query tokens of a block) begun
     // Every role walks the same passes: tiles j0..j1-1 of a sequence against one of its query tokens.
     auto walk = [&](auto&& pass) {
-        while (ok && it.next(seq, T, k0, k1)) {
+        while (ok && it.next(seq, T, k0, k1, whole)) {
             const int step = q_len > 1 ? kBlock : k1 - k0;
             for (int j0 = k0; j0 < k1 && ok; j0 += step) {
                 const int j1 = j0 + step < k1 ? j0 + step : k1;
