@@ -195,9 +195,10 @@ class Library:
             raise ValueError("cache must be a CUDA tensor")
         if cache.dim() != 3:
             raise ValueError(f"cache must have 3 dims, got {tuple(cache.shape)}")
-        if cache.stride(2) != 1:
+        shape, stride = cache.shape, cache.stride()
+        if stride[2] != 1:
             raise ValueError("cache rows must be contiguous (unit stride along the last dimension)")
-        return Cache(cache.data_ptr(), cache.shape[0], cache.shape[1], cache.stride(0), cache.stride(1))
+        return Cache(cache.data_ptr(), shape[0], shape[1], stride[0], stride[1])
 
     @staticmethod
     def opts(path=PATH_AUTO, num_pairs=0, overhead_tiles=-1, min_tiles=0, events=None, wait_limit_ns=0,
@@ -344,6 +345,15 @@ class Library:
             raise ValueError("these dims have no packed row (d_c must be a multiple of 16)")
         return n
 
+    def _row(self, dims: Dims, fmt: int) -> int:
+        """Elements of a row of that format (the packed layout of mla.h)."""
+        d_c, d_r = dims.d_c, dims.d_r
+        if fmt == CACHE_FULL:
+            return d_c + d_r
+        if d_c % 16:
+            raise ValueError("these dims have no packed row (d_c must be a multiple of 16)")
+        return ((((d_c // 2 + d_c // 16 + 15) & ~15) + d_r * (4 if dims.dtype == MLA_DTYPE_F32 else 2)) + 15) & ~15
+
     def _any_cache(self, dims: Dims, cache: torch.Tensor, device, name: str = "cache", want: Optional[int] = None):
         """(descriptor, format) of a full-width or (uint8) packed cache; ``want``: the one format the call takes."""
         fmt = CACHE_PACKED if cache.dtype is torch.uint8 else CACHE_FULL
@@ -351,12 +361,12 @@ class Library:
             raise TypeError(f"{name} must be {self._dtype(dims)} or torch.uint8 (packed), got {cache.dtype}")
         if want is not None and fmt != want:
             raise TypeError(f"the call takes a {('full-width', 'packed (torch.uint8)')[want]} cache, got {cache.dtype}")
-        d = self.cache_desc(cache)
-        row = self.packed_row_bytes(dims) if fmt == CACHE_PACKED else dims.d_c + dims.d_r
-        if cache.shape[2] < row:
-            raise ValueError(f"{name} rows hold {cache.shape[2]} elements, {row} are needed")
         if cache.device != device:
             raise ValueError(f"{name} is on {cache.device}, the other tensors on {device}")
+        d = self.cache_desc(cache)
+        row = self._row(dims, fmt)
+        if cache.shape[2] < row:
+            raise ValueError(f"{name} rows hold {cache.shape[2]} elements, {row} are needed")
         return d, fmt
 
     def _append(self, fn, want, dims, cache, c_kv, k_rope, pos, rows, stream):

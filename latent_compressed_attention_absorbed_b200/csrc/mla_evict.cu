@@ -34,6 +34,7 @@ namespace cg = cooperative_groups;
 
 constexpr int kSelThreads = 1024;
 constexpr int kSelBins = 2048;
+constexpr int kSlab = 16;  // rows a thread of the selection holds
 constexpr int kMoveThreads = 256;
 constexpr int kMovePieces = 8;  // 16-byte pieces a thread holds: chunks of up to 32 KB
 
@@ -87,11 +88,13 @@ __device__ __forceinline__ void block_scan2(int& a, int& b, int2* warp_sums, int
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictArgs a, EvictScratch s) {
     __shared__ int hist[kSelBins];
     __shared__ int2 warp_sums[32];
-    __shared__ int2 mine;          // this CTA's counts, read by the others
-    __shared__ int found[2];       // digit, keys above it
+    __shared__ int2 mine;     // this CTA's counts, read by the others
+    __shared__ int found[2];  // digit, keys above it
     cg::cluster_group cluster = cg::this_cluster();
     const int ranks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
     const int b = blockIdx.x / ranks, tid = threadIdx.x;
+    sm100::pdl_wait();
+    sm100::pdl_trigger();
     const int T = a.seqlens[b];
     const bool bad = T < 0 || T > a.T_max;
     if (blockIdx.x == 0 && tid == 0) *s.ticket = 0;
@@ -110,8 +113,49 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictArgs a, 
         const int lo = a.n_sink, hi = T - a.n_recent;  // the middle
         const int m = a.budget - a.n_sink - a.n_recent;
         const float* w = a.weights + (size_t)b * a.stride_w;
+        const bool wide = (reinterpret_cast<uintptr_t>(w) & 15) == 0;
+        // This CTA's rows, and a slab of them in registers: `each` consecutive
+        // rows a thread.  One slab holds all of them up to 16384 rows a CTA, so
+        // that the weights are read once; beyond that every pass reads them
+        // again, from L2.
+        const int64_t per = (((int64_t)T + ranks - 1) / ranks + 3) & ~int64_t(3);
+        const int64_t t_lo = min((int64_t)T, rank * per), t_hi = min((int64_t)T, t_lo + per);
+        const int slabs = (int)((per + kSlab * kSelThreads - 1) / (kSlab * kSelThreads));
+        const int each = slabs > 1 ? kSlab : (int)((per + 4 * kSelThreads - 1) / (4 * kSelThreads)) * 4;
+        uint32_t key[kSlab];
+        uint32_t middle = 0, there = 0;  // which of them are in the middle, which are rows at all
+        int held = -1;
+        auto load_slab = [&](int slab) {
+            if (held == slab) return;
+            held = slab;
+            middle = there = 0;
+            const int64_t t0 = t_lo + ((int64_t)slab * kSelThreads + tid) * each;
+#pragma unroll
+            for (int v = 0; v < kSlab / 4; ++v) {
+                const int64_t t = t0 + 4 * v;
+                float x[4] = {0.f, 0.f, 0.f, 0.f};
+                if (4 * v < each && t < t_hi) {
+                    if (wide && t + 4 <= t_hi) {
+                        const float4 f = *reinterpret_cast<const float4*>(w + t);
+                        x[0] = f.x; x[1] = f.y; x[2] = f.z; x[3] = f.w;
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            if (t + j < t_hi) x[j] = w[t + j];
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    key[4 * v + j] = weight_key(x[j]);
+                    if (4 * v < each && t + j < t_hi) {
+                        there |= 1u << (4 * v + j);
+                        if (t + j >= lo && t + j < hi) middle |= 1u << (4 * v + j);
+                    }
+                }
+            }
+        };
         // ---- the m-th largest key of the middle
-        uint32_t key = 0xFFFFFFFFu;
+        uint32_t last = 0xFFFFFFFFu;
         int equal_left = 0;  // how many of the keys equal to it stay
         if (m > 0) {
             uint32_t prefix = 0;
@@ -123,18 +167,23 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictArgs a, 
                 shift -= bits;
                 for (int i = tid; i < kSelBins; i += kSelThreads) hist[i] = 0;
                 __syncthreads();
-                for (int64_t t = lo + (int64_t)rank * kSelThreads + tid; t < hi; t += (int64_t)ranks * kSelThreads) {
-                    const uint32_t k = weight_key(w[t]);
-                    if (((k ^ prefix) & above) == 0) atomicAdd(&hist[(k >> shift) & ((1 << bits) - 1)], 1);
+                for (int slab = 0; slab < slabs; ++slab) {
+                    load_slab(slab);
+#pragma unroll
+                    for (int i = 0; i < kSlab; ++i)
+                        if ((middle >> i & 1) && ((key[i] ^ prefix) & above) == 0)
+                            atomicAdd(&hist[(key[i] >> shift) & ((1 << bits) - 1)], 1);
                 }
-                cluster.sync();
+                if (ranks > 1) cluster.sync();
+                else __syncthreads();
                 // two bins a thread, from the highest digit down
                 int c0 = 0, c1 = 0;
                 const int d0 = kSelBins - 1 - 2 * tid;
                 for (int r = 0; r < ranks; ++r) {
                     const int* other = cluster.map_shared_rank(hist, r);
-                    c0 += other[d0];
-                    c1 += other[d0 - 1];
+                    const int2 two = *reinterpret_cast<const int2*>(other + d0 - 1);
+                    c0 += two.y;
+                    c1 += two.x;
                 }
                 int before = c0 + c1, none = 0;
                 int2 total;
@@ -146,54 +195,66 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictArgs a, 
                     found[0] = d0 - 1;
                     found[1] = before + c0;
                 }
-                cluster.sync();  // every CTA has read the counts; found is set
+                // every CTA has read the counts; found is set
+                if (ranks > 1) cluster.sync();
+                else __syncthreads();
                 prefix |= (uint32_t)found[0] << shift;
                 need -= found[1];
                 __syncthreads();
             }
-            key = prefix;
+            last = prefix;
             equal_left = need;
         }
-        // ---- the kept rows in order: each CTA lists a contiguous range
-        const int64_t per = ((int64_t)T + ranks - 1) / ranks;
-        const int64_t t0 = rank * per < T ? rank * per : T, t1 = t0 + per < T ? t0 + per : T;
-        int over = 0, equal = 0;
-        for (int64_t t = t0 + tid; t < t1; t += kSelThreads) {
-            if (t < lo || t >= hi) ++over;
-            else if (m > 0) {
-                const uint32_t k = weight_key(w[t]);
-                over += k > key;
-                equal += k == key;
-            }
-        }
-        int2 total;
-        block_scan2(over, equal, warp_sums, total);
-        if (tid == 0) mine = total;
-        cluster.sync();
-        int base_over = 0, base_equal = 0;
-        for (int r = 0; r < rank; ++r) {
-            const int2 o = *cluster.map_shared_rank(&mine, r);
-            base_over += o.x;
-            base_equal += o.y;
-        }
-        for (int64_t t = t0; t < t1; t += kSelThreads) {
-            const int64_t at = t + tid;
-            int is_over = 0, is_equal = 0;
-            if (at < t1) {
-                if (at < lo || at >= hi) is_over = 1;
-                else if (m > 0) {
-                    const uint32_t k = weight_key(w[at]);
-                    is_over = k > key;
-                    is_equal = k == key;
+        // ---- the kept rows in order.  over: rows that stay whatever else does; equal: rows of the last weight.
+        auto classify = [&](uint32_t& over, uint32_t& equal) {
+            over = there & ~middle;
+            equal = 0;
+            if (m > 0) {
+#pragma unroll
+                for (int i = 0; i < kSlab; ++i) {
+                    if (key[i] > last) over |= middle & (1u << i);
+                    if (key[i] == last) equal |= middle & (1u << i);
                 }
             }
-            int x = is_over, y = is_equal;
+        };
+        int base_over = 0, base_equal = 0;
+        uint32_t over, equal;
+        int2 total;
+        if (ranks > 1) {  // what the CTAs before this one keep
+            int x = 0, y = 0;
+            for (int slab = 0; slab < slabs; ++slab) {
+                load_slab(slab);
+                classify(over, equal);
+                x += __popc(over);
+                y += __popc(equal);
+            }
             block_scan2(x, y, warp_sums, total);
-            const int eq_before = base_equal + y;
-            if (is_over || (is_equal && eq_before < equal_left)) {
-                const int slot = base_over + x + (eq_before < equal_left ? eq_before : equal_left);
-                kept[slot] = (int32_t)at;
-                if (kept_out) kept_out[slot] = (int32_t)at;
+            if (tid == 0) mine = total;
+            cluster.sync();
+            for (int r = 0; r < rank; ++r) {
+                const int2 o = *cluster.map_shared_rank(&mine, r);
+                base_over += o.x;
+                base_equal += o.y;
+            }
+        }
+        for (int slab = 0; slab < slabs; ++slab) {
+            load_slab(slab);
+            classify(over, equal);
+            int x = __popc(over), y = __popc(equal);
+            block_scan2(x, y, warp_sums, total);
+            x += base_over;
+            y += base_equal;
+            const int64_t t0 = t_lo + ((int64_t)slab * kSelThreads + tid) * each;
+#pragma unroll
+            for (int i = 0; i < kSlab; ++i) {
+                const bool is_over = over >> i & 1, is_equal = equal >> i & 1;
+                if (is_over || (is_equal && y < equal_left)) {
+                    const int slot = x + min(y, equal_left);
+                    kept[slot] = (int32_t)(t0 + i);
+                    if (kept_out) kept_out[slot] = (int32_t)(t0 + i);
+                }
+                x += is_over;
+                y += is_equal;
             }
             base_over += total.x;
             base_equal += total.y;
@@ -213,6 +274,8 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(EvictArgs a, E
     __shared__ int s_ticket;
     __shared__ int s_wait[2];
     const int tid = threadIdx.x;
+    sm100::pdl_wait();
+    sm100::pdl_trigger();
     if (tid == 0) s_ticket = a.in_place ? atomicAdd(s.ticket, 1) : (int)blockIdx.x;
     __syncthreads();
     const int b = s_ticket / s.chunks, chunk = s_ticket % s.chunks;
@@ -317,30 +380,18 @@ cudaError_t evict_launch(const EvictArgs& a, void* workspace, cudaStream_t st) {
     evict_layout(a.B, a.budget, a.row_bytes, &s, workspace);
     const int64_t blocks = (int64_t)a.B * s.chunks;
     if (blocks > INT_MAX) return cudaErrorInvalidValue;
-    // One CTA up to 8192 rows (eight rows a thread), eight above: the passes
-    // of a single CTA would read the weights at one SM's share of L2.
+    // One CTA a sequence up to 8192 rows (eight a thread), eight above: a single
+    // CTA's shared-memory counters and its share of L2 would hold it up, while
+    // the eight meetings of a cluster cost about 8 us.
     const int ranks = a.T_max <= 8 * kSelThreads ? 1 : 8;
-    cudaLaunchConfig_t cfg;
-    memset(&cfg, 0, sizeof(cfg));
-    cfg.gridDim = dim3((unsigned)(a.B * ranks));
-    cfg.blockDim = dim3(kSelThreads);
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = ranks;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, evict_select_kernel, a, s);
+    cudaError_t e = launch_pdl(evict_select_kernel, dim3((unsigned)(a.B * ranks)), dim3(kSelThreads), 0, st, ranks, a, s);
     if (e != cudaSuccess) return e;
     const dim3 grid((unsigned)blocks), block(kMoveThreads);
     switch (unit_bytes(a.row_bytes)) {
-        case 16: evict_move_kernel<uint4><<<grid, block, 0, st>>>(a, s); break;
-        case 4: evict_move_kernel<uint32_t><<<grid, block, 0, st>>>(a, s); break;
-        default: evict_move_kernel<uint16_t><<<grid, block, 0, st>>>(a, s); break;
+        case 16: return launch_pdl(evict_move_kernel<uint4>, grid, block, 0, st, 1, a, s);
+        case 4: return launch_pdl(evict_move_kernel<uint32_t>, grid, block, 0, st, 1, a, s);
+        default: return launch_pdl(evict_move_kernel<uint16_t>, grid, block, 0, st, 1, a, s);
     }
-    return cudaGetLastError();
 }
 
 }  // namespace mla

@@ -11,6 +11,7 @@
 #include "mla_packed.cuh"
 #include "mla_packed_internal.h"
 #include "mla_rope.cuh"
+#include "sm100_unpack.cuh"
 
 namespace mla {
 namespace {
@@ -72,10 +73,70 @@ __device__ __forceinline__ bool row_and_pos(const int32_t* pos, const int32_t* r
     return true;
 }
 
+// Codes and scale of the 16 latents at src.  4 bits cannot hold a NaN or an
+// infinity: a NaN is stored as 0, what is above 13440 as the largest level, and
+// `odd` is set.
+__device__ __forceinline__ void quantise_group(const float* src, uint32_t (&w)[2], uint32_t& code, bool& odd) {
+    float x[16], amax = 0.f;
+    ld16(src, x);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+        if (!(fabsf(x[e]) <= 13440.0f)) {
+            odd = true;
+            x[e] = x[e] > 0.f ? 13440.0f : (x[e] < 0.f ? -13440.0f : 0.f);
+        }
+        amax = fmaxf(amax, fabsf(x[e]));
+    }
+    code = packed_scale_code(amax);
+    const float s = packed_scale(code), inv = 1.0f / s;
+    w[0] = w[1] = 0;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) w[e / 8] |= (uint32_t)(packed_quantise(x[e], s, inv) + 8) << packed_shift(e & 7);
+}
+__device__ __forceinline__ void quantise_group(const __nv_bfloat16* src, uint32_t (&w)[2], uint32_t& code, bool& odd) {
+    uint32_t v[8];
+    const uint4 lo = __ldg(reinterpret_cast<const uint4*>(src)), hi = __ldg(reinterpret_cast<const uint4*>(src) + 1);
+    v[0] = lo.x; v[1] = lo.y; v[2] = lo.z; v[3] = lo.w;
+    v[4] = hi.x; v[5] = hi.y; v[6] = hi.z; v[7] = hi.w;
+    // magnitudes compare as integers, and a NaN is larger than an infinity
+    uint32_t top = v[0] & 0x7FFF7FFFu;
+#pragma unroll
+    for (int j = 1; j < 8; ++j) top = __vmaxu2(top, v[j] & 0x7FFF7FFFu);
+    const uint32_t mag = max(top & 0xFFFFu, top >> 16);
+    float amax = __uint_as_float(mag << 16);
+    if (mag > 0x4652u) {  // 13440
+        odd = true;
+        amax = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            uint32_t fixed = 0;
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                uint32_t b = (v[j] >> (16 * half)) & 0xFFFFu;
+                if ((b & 0x7FFFu) > 0x7F80u) b = 0;
+                else if ((b & 0x7FFFu) > 0x4652u) b = (b & 0x8000u) | 0x4652u;
+                amax = fmaxf(amax, __uint_as_float((b & 0x7FFFu) << 16));
+                fixed |= b << (16 * half);
+            }
+            v[j] = fixed;
+        }
+    }
+    code = packed_scale_code(amax);
+    const float inv = 1.0f / packed_scale(code);
+    w[0] = w[1] = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {  // elements 2j and 2j + 1
+        w[j / 4] |= packed_code_bf16(__uint_as_float(v[j] << 16), inv) << (4 * (j & 3));
+        w[j / 4] |= packed_code_bf16(__uint_as_float(v[j] & 0xFFFF0000u), inv) << (4 * (j & 3) + 16);
+    }
+}
+
 // A warp quantises one token.  Each lane owns whole groups of 16 latents (one
 // each at d_c = 512), so the group's maximum needs no exchange between lanes,
-// and the warp's stores of codes, scales and key are contiguous.  Bound by
-// HBM: 1152 bytes read and 416 written a token in bf16.
+// and the warp's stores of codes, scales and key are contiguous.  1152 bytes
+// are read and 416 written a token in bf16; the arithmetic (five instructions
+// a latent in bf16, and the rotation of the key) is kept small enough for that
+// to be the bound.
 template <typename T>
 __global__ void __launch_bounds__(kRowWarps * 32)
     append_packed_kernel(const T* __restrict__ c_kv, const T* __restrict__ k_rope, const int32_t* __restrict__ pos,
@@ -89,28 +150,10 @@ __global__ void __launch_bounds__(kRowWarps * 32)
     if (!row_and_pos(pos, rows, b, i, n_tok, cache.T_max, lane, status, &r, &p)) return;
     const PackedLayout l = packed_layout(d_c, d_r, sizeof(T));
     uint8_t* row = static_cast<uint8_t*>(cache.data) + (int64_t)b * cache.stride_b + (int64_t)r * cache.stride_t;
-    const T* src = c_kv + gw * d_c;
     bool odd = false;
     for (int g = lane; g < d_c / kPackGroup; g += 32) {
-        float x[16];
-        ld16(src + g * kPackGroup, x);
-        float amax = 0.f;
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-            // 4 bits cannot hold a NaN or an infinity: a NaN is stored as 0, what
-            // is too large as the largest level, and the status word tells.
-            if (!(fabsf(x[e]) <= 13440.0f)) {
-                odd = true;
-                x[e] = x[e] > 0.f ? 13440.0f : (x[e] < 0.f ? -13440.0f : 0.f);
-            }
-            amax = fmaxf(amax, fabsf(x[e]));
-        }
-        const uint32_t code = packed_scale_code(amax);
-        const float s = packed_scale(code), inv = 1.0f / s;
-        uint32_t w[2] = {0, 0};
-#pragma unroll
-        for (int e = 0; e < 16; ++e)
-            w[e / 8] |= (uint32_t)(packed_quantise(x[e], s, inv) + 8) << packed_shift(e & 7);
+        uint32_t w[2], code;
+        quantise_group(c_kv + gw * d_c + g * kPackGroup, w, code, odd);
         reinterpret_cast<uint2*>(row)[g] = make_uint2(w[0], w[1]);
         row[l.off_scale + g] = (uint8_t)code;
     }
@@ -175,6 +218,14 @@ __global__ void __launch_bounds__(kRowWarps * 32)
     const bool wide = ((d_c + d_r) * sizeof(T)) % 16 == 0;
     for (int g = lane; g < d_c / kPackGroup; g += 32) {
         const uint2 w2 = reinterpret_cast<const uint2*>(row)[g];
+        if (sizeof(T) == 2 && wide) {
+            uint32_t v[8];
+            sm100::unpack16<false>(w2.x, w2.y, row[l.off_scale + g], v);
+            uint4* to = reinterpret_cast<uint4*>(dst + g * kPackGroup);
+            to[0] = make_uint4(v[0], v[1], v[2], v[3]);
+            to[1] = make_uint4(v[4], v[5], v[6], v[7]);
+            continue;
+        }
         const float s = packed_scale(row[l.off_scale + g]);
         float x[16];
 #pragma unroll

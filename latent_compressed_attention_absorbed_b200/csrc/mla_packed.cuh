@@ -72,6 +72,17 @@ __device__ __forceinline__ int packed_quantise(float x, float s, float inv_s) {
     return (int)fminf(fmaxf(q, -7.0f), 7.0f);
 }
 
+// The same for x with eight significant bits (a bf16 value), as q + 8 in the
+// low four bits.  Where |x / s| is at least 0.4, x / s is a multiple of 2^-7 / S
+// with S the scale's four bits, so it is either exactly a half or at least
+// 5e-4 away from one: rounded to a multiple of 2^-13 (the unit in the last
+// place at 1536) the product with the rounded reciprocal falls on a half
+// exactly where x / s does, and the addition then rounds halves to even.
+__device__ __forceinline__ uint32_t packed_code_bf16(float x, float inv_s) {
+    const float snapped = fmaf(x, inv_s, 1536.0f);
+    return __float_as_uint(snapped + (12582912.0f + 8.0f - 1536.0f)) & 15u;  // 1.5 * 2^23: the unit in the last place is 1
+}
+
 // Word bit position of element e (0..7) of a word.
 __host__ __device__ constexpr int packed_shift(int e) { return 4 * (e >> 1) + 16 * (e & 1); }
 
