@@ -6,12 +6,14 @@
 // with the largest weights stay, in their order.  Equal weights: the lower
 // row; -0 equals 0, a NaN counts as less than every number.
 //
-// evict_select_kernel: a cluster of CTAs per sequence finds the m-th largest
-// weight by a radix search over order-preserving 32-bit keys (three passes of
-// 11, 11 and 10 bits: each pass counts the digits of the keys that share the
-// prefix found so far, in shared memory, and the CTAs add their counts up
+// evict_select_kernel: a cluster of CTAs per sequence finds the last weight
+// that stays by a radix search over order-preserving 32-bit keys (up to three
+// passes of 11, 11 and 10 bits: each counts the digits of the keys that share
+// the prefix found so far, in shared memory, and the CTAs add their counts up
 // through distributed shared memory), then lists the kept rows in order with
-// one prefix sum.  The weights are read from HBM once; the later passes hit L2.
+// one prefix sum.  The first and last rows take part with a key above every
+// weight's.  A thread keeps its rows' keys in registers, so the weights are
+// read once.
 // evict_move_kernel: a CTA moves a chunk of kept rows.  It is bound by HBM:
 // every kept row is read once and written once.
 // In place, a kept row never moves to a higher index, and the rows that a
@@ -32,17 +34,20 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kSelThreads = 1024;
 constexpr int kSelBins = 2048;
+constexpr int kSelRanks = 8;  // CTAs of a cluster
 constexpr int kSlab = 16;  // rows a thread of the selection holds
 constexpr int kMoveThreads = 256;
 constexpr int kMovePieces = 8;  // 16-byte pieces a thread holds: chunks of up to 32 KB
 
-// Larger weight <-> larger key; NaN 0, -0 as 0.
+// Larger weight <-> larger key, -0 as 0.  No number maps below 0x007FFFFF or
+// above 0xFF800000: a NaN is 1, a row that stays in any case (the first and the
+// last ones) kKeySafe, no row 0.
+constexpr uint32_t kKeyNaN = 1u, kKeySafe = 0xFFFFFFFFu;
 __device__ __forceinline__ uint32_t weight_key(float w) {
-    if (w != w) return 0u;
     const uint32_t u = __float_as_uint(w + 0.0f);
-    return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+    const uint32_t k = u ^ (uint32_t)(((int32_t)u >> 31) | 0x80000000);
+    return w != w ? kKeyNaN : k;
 }
 
 struct EvictScratch {
@@ -53,211 +58,236 @@ struct EvictScratch {
     int chunks, chunk_rows;
 };
 
-// Block-wide exclusive prefix of two counts; `total` gets their sums.
-__device__ __forceinline__ void block_scan2(int& a, int& b, int2* warp_sums, int2& total) {
+// Block-wide exclusive prefix of a count (or two packed ones); `total` gets the
+// sum.  One barrier; `sums` must not be in use by a scan one barrier ago.
+template <int kWarps>
+__device__ __forceinline__ uint64_t block_scan(uint64_t v, uint64_t* sums, uint64_t& total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int x = a, y = b;
+    uint64_t x = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int x1 = __shfl_up_sync(0xffffffffu, x, o), y1 = __shfl_up_sync(0xffffffffu, y, o);
-        if (lane >= o) {
-            x += x1;
-            y += y1;
-        }
+        const uint64_t y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
     }
-    __syncthreads();  // warp_sums of the previous scan have been read
-    if (lane == 31) warp_sums[warp] = make_int2(x, y);
+    if (lane == 31) sums[warp] = x;
     __syncthreads();
-    int2 w = warp_sums[lane];  // 32 warps
-    int wx = w.x, wy = w.y;
+    const uint64_t mine = lane < kWarps ? sums[lane] : 0;
+    uint64_t w = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int x1 = __shfl_up_sync(0xffffffffu, wx, o), y1 = __shfl_up_sync(0xffffffffu, wy, o);
-        if (lane >= o) {
-            wx += x1;
-            wy += y1;
-        }
+        const uint64_t y = __shfl_up_sync(0xffffffffu, w, o);
+        if (lane >= o) w += y;
     }
-    total = make_int2(__shfl_sync(0xffffffffu, wx, 31), __shfl_sync(0xffffffffu, wy, 31));
-    const int bx = __shfl_sync(0xffffffffu, wx - w.x, warp), by = __shfl_sync(0xffffffffu, wy - w.y, warp);
-    const int ax = x - a, ay = y - b;
-    a = bx + ax;
-    b = by + ay;
+    total = __shfl_sync(0xffffffffu, w, 31);
+    return __shfl_sync(0xffffffffu, w - mine, warp) + x - v;
 }
 
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictArgs a, EvictScratch s) {
-    __shared__ int hist[kSelBins];
-    __shared__ int2 warp_sums[32];
-    __shared__ int2 mine;     // this CTA's counts, read by the others
-    __shared__ int found[2];  // digit, keys above it
+template <int kThreads>
+__global__ void __launch_bounds__(kThreads) evict_select_kernel(EvictArgs a, EvictScratch s) {
+    constexpr int kWarps = kThreads / 32, kBins = kSelBins / kThreads;  // bins a thread
+    __shared__ __align__(16) int hist[3][kSelBins];  // one for each pass: a pass needs no second meeting to clear it
+    __shared__ uint64_t sums[2][32];
+    __shared__ uint64_t mine;    // this CTA's counts, read by the others
+    __shared__ int found[3][3];  // of each pass: digit, keys above it, keys with it
     cg::cluster_group cluster = cg::this_cluster();
     const int ranks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
-    const int b = blockIdx.x / ranks, tid = threadIdx.x;
+    const int b = blockIdx.x / ranks, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     sm100::pdl_wait();
     sm100::pdl_trigger();
     const int T = a.seqlens[b];
     const bool bad = T < 0 || T > a.T_max;
     if (blockIdx.x == 0 && tid == 0) *s.ticket = 0;
     if (rank == 0)
-        for (int c = tid; c < s.chunks; c += kSelThreads) s.loaded[(size_t)b * s.chunks + c] = 0;
+        for (int c = tid; c < s.chunks; c += kThreads) s.loaded[(size_t)b * s.chunks + c] = 0;
     const int n = bad ? 0 : (T < a.budget ? T : a.budget);
     int32_t* kept = s.kept + (size_t)b * a.budget;
     int32_t* kept_out = a.kept_out ? a.kept_out + (size_t)b * a.budget : nullptr;
     if (bad || T <= a.budget) {  // the same for the whole cluster
         if (bad && rank == 0 && tid == 0) atomicOr(a.status, MLA_STATUS_BAD_SEQLEN);
-        for (int j = rank * kSelThreads + tid; j < a.budget; j += ranks * kSelThreads) {
+        for (int j = rank * kThreads + tid; j < a.budget; j += ranks * kThreads) {
             if (j < n) kept[j] = j;
             if (kept_out) kept_out[j] = j < n ? j : -1;
         }
     } else {
         const int lo = a.n_sink, hi = T - a.n_recent;  // the middle
-        const int m = a.budget - a.n_sink - a.n_recent;
         const float* w = a.weights + (size_t)b * a.stride_w;
         const bool wide = (reinterpret_cast<uintptr_t>(w) & 15) == 0;
-        // This CTA's rows, and a slab of them in registers: `each` consecutive
-        // rows a thread.  One slab holds all of them up to 16384 rows a CTA, so
-        // that the weights are read once; beyond that every pass reads them
-        // again, from L2.
+        // This CTA's rows, and a slab of their keys in registers: a warp has 32
+        // `each` consecutive rows, its lanes four at a time in turn (so that loads
+        // and the kept rows' stores stay within a few lines).  One slab holds all
+        // of them up to 16 rows a thread, and the weights are read once; beyond
+        // that every pass reads them again, from L2.
         const int64_t per = (((int64_t)T + ranks - 1) / ranks + 3) & ~int64_t(3);
         const int64_t t_lo = min((int64_t)T, rank * per), t_hi = min((int64_t)T, t_lo + per);
-        const int slabs = (int)((per + kSlab * kSelThreads - 1) / (kSlab * kSelThreads));
-        const int each = slabs > 1 ? kSlab : (int)((per + 4 * kSelThreads - 1) / (4 * kSelThreads)) * 4;
+        const int slabs = (int)((per + kSlab * kThreads - 1) / (kSlab * kThreads));
+        const int each = slabs > 1 ? kSlab : (int)((per + 4 * kThreads - 1) / (4 * kThreads)) * 4;
         uint32_t key[kSlab];
-        uint32_t middle = 0, there = 0;  // which of them are in the middle, which are rows at all
         int held = -1;
         auto load_slab = [&](int slab) {
             if (held == slab) return;
             held = slab;
-            middle = there = 0;
-            const int64_t t0 = t_lo + ((int64_t)slab * kSelThreads + tid) * each;
+            const int64_t t0 = t_lo + ((int64_t)slab * kWarps + warp) * (32 * each) + 4 * lane;
+            float4 f[kSlab / 4];
 #pragma unroll
             for (int v = 0; v < kSlab / 4; ++v) {
-                const int64_t t = t0 + 4 * v;
-                float x[4] = {0.f, 0.f, 0.f, 0.f};
-                if (4 * v < each && t < t_hi) {
-                    if (wide && t + 4 <= t_hi) {
-                        const float4 f = *reinterpret_cast<const float4*>(w + t);
-                        x[0] = f.x; x[1] = f.y; x[2] = f.z; x[3] = f.w;
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            if (t + j < t_hi) x[j] = w[t + j];
-                    }
+                const int64_t t = t0 + 128 * v;
+                f[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (4 * v >= each || t >= t_hi) continue;
+                if (wide && t + 4 <= t_hi) {
+                    f[v] = *reinterpret_cast<const float4*>(w + t);
+                } else {
+                    f[v].x = w[t];
+                    if (t + 1 < t_hi) f[v].y = w[t + 1];
+                    if (t + 2 < t_hi) f[v].z = w[t + 2];
+                    if (t + 3 < t_hi) f[v].w = w[t + 3];
                 }
+            }
+#pragma unroll
+            for (int v = 0; v < kSlab / 4; ++v) {
+                const int64_t t = t0 + 128 * v;
+                const float x[4] = {f[v].x, f[v].y, f[v].z, f[v].w};
+                const bool inside = 4 * v < each && t >= lo && t + 4 <= hi && t + 4 <= t_hi;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    key[4 * v + j] = weight_key(x[j]);
-                    if (4 * v < each && t + j < t_hi) {
-                        there |= 1u << (4 * v + j);
-                        if (t + j >= lo && t + j < hi) middle |= 1u << (4 * v + j);
+                    uint32_t k = weight_key(x[j]);
+                    if (!inside) {
+                        if (t + j < lo || t + j >= hi) k = kKeySafe;
+                        if (4 * v >= each || t + j >= t_hi) k = 0u;
                     }
+                    key[4 * v + j] = k;
                 }
             }
         };
-        // ---- the m-th largest key of the middle
-        uint32_t last = 0xFFFFFFFFu;
-        int equal_left = 0;  // how many of the keys equal to it stay
-        if (m > 0) {
-            uint32_t prefix = 0;
-            int need = m;
-            int shift = 32;
-            for (int pass = 0; pass < 3; ++pass) {
-                const int bits = pass < 2 ? 11 : 10;
-                const uint32_t above = shift == 32 ? 0u : 0xFFFFFFFFu << shift;
-                shift -= bits;
-                for (int i = tid; i < kSelBins; i += kSelThreads) hist[i] = 0;
-                __syncthreads();
-                for (int slab = 0; slab < slabs; ++slab) {
-                    load_slab(slab);
-#pragma unroll
-                    for (int i = 0; i < kSlab; ++i)
-                        if ((middle >> i & 1) && ((key[i] ^ prefix) & above) == 0)
-                            atomicAdd(&hist[(key[i] >> shift) & ((1 << bits) - 1)], 1);
-                }
-                if (ranks > 1) cluster.sync();
-                else __syncthreads();
-                // two bins a thread, from the highest digit down
-                int c0 = 0, c1 = 0;
-                const int d0 = kSelBins - 1 - 2 * tid;
-                for (int r = 0; r < ranks; ++r) {
-                    const int* other = cluster.map_shared_rank(hist, r);
-                    const int2 two = *reinterpret_cast<const int2*>(other + d0 - 1);
-                    c0 += two.y;
-                    c1 += two.x;
-                }
-                int before = c0 + c1, none = 0;
-                int2 total;
-                block_scan2(before, none, warp_sums, total);
-                if (before < need && before + c0 >= need) {
-                    found[0] = d0;
-                    found[1] = before;
-                } else if (before + c0 < need && before + c0 + c1 >= need) {
-                    found[0] = d0 - 1;
-                    found[1] = before + c0;
-                }
-                // every CTA has read the counts; found is set
-                if (ranks > 1) cluster.sync();
-                else __syncthreads();
-                prefix |= (uint32_t)found[0] << shift;
-                need -= found[1];
-                __syncthreads();
-            }
-            last = prefix;
-            equal_left = need;
-        }
-        // ---- the kept rows in order.  over: rows that stay whatever else does; equal: rows of the last weight.
-        auto classify = [&](uint32_t& over, uint32_t& equal) {
-            over = there & ~middle;
-            equal = 0;
-            if (m > 0) {
-#pragma unroll
-                for (int i = 0; i < kSlab; ++i) {
-                    if (key[i] > last) over |= middle & (1u << i);
-                    if (key[i] == last) equal |= middle & (1u << i);
-                }
-            }
-        };
-        int base_over = 0, base_equal = 0;
-        uint32_t over, equal;
-        int2 total;
-        if (ranks > 1) {  // what the CTAs before this one keep
-            int x = 0, y = 0;
+        // ---- the key of the budget-th row from above: `last`, of whose equals equal_left stay
+        for (int i = tid; i < 3 * kSelBins; i += kThreads) (&hist[0][0])[i] = 0;
+        __syncthreads();
+        uint32_t last = 0u;
+        int need = a.budget;
+        int shift = 32;
+#pragma unroll 1
+        for (int pass = 0; pass < 3; ++pass) {
+            const int bits = pass < 2 ? 11 : 10;
+            const uint32_t above = shift == 32 ? 0u : 0xFFFFFFFFu << shift;
+            shift -= bits;
+            const uint32_t digits = (1u << bits) - 1;
             for (int slab = 0; slab < slabs; ++slab) {
                 load_slab(slab);
-                classify(over, equal);
-                x += __popc(over);
-                y += __popc(equal);
+#pragma unroll
+                for (int i = 0; i < kSlab; ++i)
+                    if (i < each && ((key[i] ^ last) & above) == 0) atomicAdd(&hist[pass][(key[i] >> shift) & digits], 1);
             }
-            block_scan2(x, y, warp_sums, total);
-            if (tid == 0) mine = total;
-            cluster.sync();
-            for (int r = 0; r < rank; ++r) {
-                const int2 o = *cluster.map_shared_rank(&mine, r);
-                base_over += o.x;
-                base_equal += o.y;
+            if (ranks > 1) cluster.sync();
+            else __syncthreads();
+            // kBins bins a thread, from the highest digit down
+            int c[kBins];
+            const int top = kSelBins - 1 - kBins * tid;
+#pragma unroll
+            for (int k = 0; k < kBins; ++k) c[k] = 0;
+#pragma unroll
+            for (int r = 0; r < kSelRanks; ++r) {  // (unrolled, so that the remote reads overlap)
+                if (r >= ranks) break;
+                const int* other = cluster.map_shared_rank(&hist[pass][0], r) + top - (kBins - 1);
+#pragma unroll
+                for (int k = 0; k < kBins; k += 2) {
+                    const int2 two = *reinterpret_cast<const int2*>(other + kBins - 2 - k);
+                    c[k] += two.y;
+                    c[k + 1] += two.x;
+                }
+            }
+            int sum = 0;
+#pragma unroll
+            for (int k = 0; k < kBins; ++k) sum += c[k];
+            uint64_t total;
+            int before = (int)block_scan<kWarps>(sum, sums[pass & 1], total);
+            if (before < need && before + sum >= need) {
+#pragma unroll
+                for (int k = 0; k < kBins; ++k) {
+                    if (before < need && before + c[k] >= need) {
+                        found[pass][0] = top - k;
+                        found[pass][1] = before;
+                        found[pass][2] = c[k];
+                    }
+                    before += c[k];
+                }
+            }
+            __syncthreads();
+            last |= (uint32_t)found[pass][0] << shift;
+            need -= found[pass][1];
+            if (found[pass][2] == need && last > 0u) {  // all rows with this digit stay: everything from `last` up
+                --last;
+                need = 0;
+                break;
             }
         }
-        for (int slab = 0; slab < slabs; ++slab) {
-            load_slab(slab);
-            classify(over, equal);
-            int x = __popc(over), y = __popc(equal);
-            block_scan2(x, y, warp_sums, total);
-            x += base_over;
-            y += base_equal;
-            const int64_t t0 = t_lo + ((int64_t)slab * kSelThreads + tid) * each;
+        const int equal_left = need;
+        // ---- the kept rows in order.  Counts are pairs: rows above the last key in the low half, rows with it in the high half.
+        uint32_t over = 0, equal = 0;  // which of this lane's rows
+        auto classify = [&]() {
+            over = equal = 0;
 #pragma unroll
             for (int i = 0; i < kSlab; ++i) {
-                const bool is_over = over >> i & 1, is_equal = equal >> i & 1;
-                if (is_over || (is_equal && y < equal_left)) {
-                    const int slot = x + min(y, equal_left);
-                    kept[slot] = (int32_t)(t0 + i);
-                    if (kept_out) kept_out[slot] = (int32_t)(t0 + i);
-                }
-                x += is_over;
-                y += is_equal;
+                over |= key[i] > last ? 1u << i : 0u;
+                equal |= key[i] == last ? 1u << i : 0u;
             }
-            base_over += total.x;
-            base_equal += total.y;
+        };
+        auto warp_count = [&]() {  // (a warp's slab has 512 rows)
+            const uint32_t c = __reduce_add_sync(0xffffffffu, (uint32_t)(__popc(equal) << 16 | __popc(over)));
+            return (uint64_t)(c >> 16) << 32 | (c & 0xFFFFu);
+        };
+        uint64_t base = 0, total;
+        __syncthreads();  // the last pass has read its sums
+        if (ranks > 1) {  // what the CTAs before this one keep
+            uint64_t own = 0;
+            for (int slab = 0; slab < slabs; ++slab) {
+                load_slab(slab);
+                classify();
+                own += warp_count();
+            }
+            block_scan<kWarps>(lane == 0 ? own : 0, sums[1], total);
+            if (tid == 0) mine = total;
+            cluster.sync();
+#pragma unroll
+            for (int r = 0; r < kSelRanks; ++r)
+                if (r < rank) base += *cluster.map_shared_rank(&mine, r);
+        }
+        for (int slab = 0; slab < slabs; ++slab) {
+            if (slabs > 1 || ranks == 1) {
+                load_slab(slab);
+                classify();
+            }
+            const uint64_t own = warp_count();
+            uint64_t at = block_scan<kWarps>(lane == 0 ? own : 0, sums[slab & 1], total);
+            at = base + __shfl_sync(0xffffffffu, at, 0);
+            base += total;
+            if (own == 0) continue;
+            const int t0 = (int)(t_lo + ((int64_t)slab * kWarps + warp) * (32 * each) + 4 * lane);
+#pragma unroll
+            for (int v = 0; v < kSlab / 4; ++v) {
+                if (4 * v >= each) break;
+                const uint32_t o4 = over >> (4 * v) & 15u, e4 = equal >> (4 * v) & 15u;
+                const uint32_t c = __popc(e4) << 16 | __popc(o4);
+                uint32_t inc = c;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const uint32_t up = __shfl_up_sync(0xffffffffu, inc, o);
+                    if (lane >= o) inc += up;
+                }
+                int x = (int)(uint32_t)at + (int)((inc - c) & 0xFFFFu), y = (int)(at >> 32) + (int)((inc - c) >> 16);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const bool is_over = o4 >> j & 1, is_equal = e4 >> j & 1;
+                    const int slot = x + min(y, equal_left);
+                    // (slot < budget holds for weights that nobody changes meanwhile)
+                    if ((is_over || (is_equal && y < equal_left)) && slot < a.budget) {
+                        kept[slot] = t0 + 128 * v + j;
+                        if (kept_out) kept_out[slot] = t0 + 128 * v + j;
+                    }
+                    x += is_over;
+                    y += is_equal;
+                }
+                const uint32_t all = __shfl_sync(0xffffffffu, inc, 31);
+                at += (uint64_t)(all >> 16) << 32 | (all & 0xFFFFu);
+            }
         }
     }
     // seqlens_out may be seqlens: every CTA of the cluster has read it by now,
@@ -380,11 +410,12 @@ cudaError_t evict_launch(const EvictArgs& a, void* workspace, cudaStream_t st) {
     evict_layout(a.B, a.budget, a.row_bytes, &s, workspace);
     const int64_t blocks = (int64_t)a.B * s.chunks;
     if (blocks > INT_MAX) return cudaErrorInvalidValue;
-    // One CTA a sequence up to 8192 rows (eight a thread), eight above: a single
-    // CTA's shared-memory counters and its share of L2 would hold it up, while
-    // the eight meetings of a cluster cost about 8 us.
-    const int ranks = a.T_max <= 8 * kSelThreads ? 1 : 8;
-    cudaError_t e = launch_pdl(evict_select_kernel, dim3((unsigned)(a.B * ranks)), dim3(kSelThreads), 0, st, ranks, a, s);
+    // Up to 8192 rows a sequence is one CTA's, of 512 threads (sixteen rows each;
+    // its barriers cost less than those of 1024).  Above, eight CTAs of 1024: the
+    // loads and counters of one would hold it up.
+    cudaError_t e = a.T_max <= 512 * kSlab
+                        ? launch_pdl(evict_select_kernel<512>, dim3((unsigned)a.B), dim3(512), 0, st, 1, a, s)
+                        : launch_pdl(evict_select_kernel<1024>, dim3((unsigned)a.B * kSelRanks), dim3(1024), 0, st, kSelRanks, a, s);
     if (e != cudaSuccess) return e;
     const dim3 grid((unsigned)blocks), block(kMoveThreads);
     switch (unit_bytes(a.row_bytes)) {
