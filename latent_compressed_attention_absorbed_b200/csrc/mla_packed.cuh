@@ -13,9 +13,7 @@
 // A uniform grid of 15 levels has a smaller rms error on normally distributed
 // groups of 16 than a 4-bit floating-point grid of the same range (0.085 of
 // the rms against 0.095), and it unpacks with one fused multiply-add for two
-// values: with the code shifted under the exponent of 16, the half word reads
-// 16 + n, and (16 + n) s - 24 s is exact, because 24 s has six significant
-// bits and the result at most seven.  The scale has four significant bits
+// values, exactly.  The scale has four significant bits
 // (3 stored), five exponent bits and no zero, infinity or NaN, so whatever
 // bytes a row holds, the latents it stands for are finite numbers; every
 // value q s is exact in bf16 and, as a multiple of 2^-24 below 2^14, in fp16.

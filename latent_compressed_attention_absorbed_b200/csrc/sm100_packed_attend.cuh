@@ -310,6 +310,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool loader = warp <= 9;
         const int odd = loader ? 1 : 0;
         const int row = 32 * (loader ? quarter : (warp < 12 ? warp - 10 : warp - 14)) + lane;
+        const uint32_t row_at = base + kOffChunk + sw128(row, 0);
         int g = 0;
         for (int seg = 0; ok && it.next(seq, T, k0, k1, whole); ++seg) {
             if (loader) {
@@ -365,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int c = odd; c < 8; c += 2) {
                     const int slot = c % kChunks;
                     if (!wait(kChEmpty + slot, c / kChunks + 1)) { ok = false; break; }
-                    raw.unpack<false>(base + kOffChunk + slot * kChunkBytes + row * 128, row);
+                    raw.unpack<false>(row_at + slot * kChunkBytes);
                     if (c + 2 < 8) raw.load(src, c + 2);
                     fence_proxy_async_smem();
                     __syncwarp();
@@ -414,7 +415,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tmem_ld32(s_addr + j0, v);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int j = 0; j < 32; j += 2) mx = fmaxf(mx, fmaxf(__uint_as_float(v[j]), __uint_as_float(v[j + 1])));
+                        for (int j = 0; j < 32; j += 2) mx = max3(mx, __uint_as_float(v[j]), __uint_as_float(v[j + 1]));
                     }
                 }
                 float* rg = red + (sb * 2) * kHeads;
@@ -440,7 +441,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (ok && unit >= kSlots) ok = wait_peer(kSlotFree + slot, unit / kSlots + 1);
                 if (ok) {
                     const uint32_t stg = base + kOffStage + slot * kSlotBytes;
-                    float rs0 = 0.f, rs1 = 0.f;
+                    // (two values an instruction where there is one for it)
+                    const uint64_t sl2x2 = pack_f32x2(sl2, sl2), mbx2 = pack_f32x2(mb, mb);
+                    uint64_t rs = 0;
 #pragma unroll 1
                     for (int j0 = 0; j0 < kUnit; j0 += 16) {
                         uint32_t v[16], pk[8];
@@ -448,15 +451,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tmem_wait_ld();
 #pragma unroll
                         for (int j = 0; j < 8; ++j) {
-                            const float p0 = ex2(fmaf(__uint_as_float(v[2 * j]), sl2, mb));
-                            const float p1 = ex2(fmaf(__uint_as_float(v[2 * j + 1]), sl2, mb));
-                            rs0 += p0;
-                            rs1 += p1;
+                            float p0, p1;
+                            unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1])), sl2x2, mbx2), p0, p1);
+                            p0 = ex2(p0);
+                            p1 = ex2(p1);
+                            rs = add_f32x2(rs, pack_f32x2(p0, p1));
                             pk[j] = pack_f16(p0, p1);
                         }
                         st_shared_v4(stg + sw128(m, j0 / 8), pk[0], pk[1], pk[2], pk[3]);
                         st_shared_v4(stg + sw128(m, j0 / 8 + 1), pk[4], pk[5], pk[6], pk[7]);
                     }
+                    float rs0, rs1;
+                    unpack_f32x2(rs, rs0, rs1);
                     l_part += rs0 + rs1;
                     st_shared_v2(stg + kSlotP + 8 * m, __float_as_uint(kh ? 1.0f : f), __float_as_uint(l_part));
                     tc_fence_before();
@@ -536,10 +542,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 RawChunk raw;
                 raw.load(src, 2 * part);
                 if (!wait(kVEmpty + vs, u / kVStages + 1)) { ok = false; break; }
-                const uint32_t dst = base + kOffV + vs * kVBytes + 2 * part * kVChunk + row * 128;
-                raw.unpack<true>(dst, row);
+                const uint32_t dst = base + kOffV + vs * kVBytes + 2 * part * kVChunk + sw128(row, 0);
+                raw.unpack<true>(dst);
                 raw.load(src, 2 * part + 1);
-                raw.unpack<true>(dst + kVChunk, row);
+                raw.unpack<true>(dst + kVChunk);
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {

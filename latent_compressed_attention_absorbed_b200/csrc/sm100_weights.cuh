@@ -313,6 +313,7 @@ __global__ void __launch_bounds__(Cfg<kPacked>::kThreads, 1)
         float* sums = reinterpret_cast<float*>(base_ptr + C::kOffSums);
         const uint32_t nl_addr = smem_u32(nlse);
         const uint32_t s_addr = tmem + ((uint32_t)(quarter * 32) << 16) + kTmemS + kHeads * set;
+        const uint64_t sl2x2 = pack_f32x2(args.scale_log2, args.scale_log2);
         int n = 0;  // tiles of this set
         walk([&](int j0, int j1, int i) {
             __syncwarp();
@@ -325,7 +326,7 @@ __global__ void __launch_bounds__(Cfg<kPacked>::kThreads, 1)
             for (int t = j0 + set; t < j1; t += 2, ++n) {
                 if (!wait(C::kSFull + set, n)) return false;
                 tc_fence_after();
-                float w0 = 0.f, w1 = 0.f;
+                uint64_t w2 = 0;
 #pragma unroll 1
                 for (int h = 0; h < kHeads; h += 16) {
                     uint32_t v[16];
@@ -335,12 +336,18 @@ __global__ void __launch_bounds__(Cfg<kPacked>::kThreads, 1)
                     for (int j = 0; j < 16; j += 4) {
                         uint32_t z[4];
                         ld_shared_v4u(nl_addr + 4 * (h + j), z[0], z[1], z[2], z[3]);
-                        w0 += ex2(fmaf(__uint_as_float(v[j]), args.scale_log2, __uint_as_float(z[0])));
-                        w1 += ex2(fmaf(__uint_as_float(v[j + 1]), args.scale_log2, __uint_as_float(z[1])));
-                        w0 += ex2(fmaf(__uint_as_float(v[j + 2]), args.scale_log2, __uint_as_float(z[2])));
-                        w1 += ex2(fmaf(__uint_as_float(v[j + 3]), args.scale_log2, __uint_as_float(z[3])));
+#pragma unroll
+                        for (int e = 0; e < 4; e += 2) {  // (two values an instruction where there is one for it)
+                            float p0, p1;
+                            unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(v[j + e]), __uint_as_float(v[j + e + 1])), sl2x2,
+                                                   pack_f32x2(__uint_as_float(z[e]), __uint_as_float(z[e + 1]))),
+                                         p0, p1);
+                            w2 = add_f32x2(w2, pack_f32x2(ex2(p0), ex2(p1)));
+                        }
                     }
                 }
+                float w0, w1;
+                unpack_f32x2(w2, w0, w1);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(C::kSFree + set));
