@@ -69,7 +69,7 @@ struct Cfg {
         kSFull = kChEmpty + kRing,     // S of a set complete (MMA commit)
         kSFree = kSFull + 2,           // S of a set read (4 warps)
         kRawFull = kSFree + 2,         // raw rows loaded (tx)
-        kRawEmpty = kRawFull + kRawStages,  // raw rows unpacked (2 row quarters x 2 warps)
+        kRawEmpty = kRawFull + kRawStages,  // raw rows unpacked (8 warps)
         kKeyFull = kRawEmpty + kRawStages,  // keys loaded (tx)
         kKeyEmpty,                          // keys multiplied (MMA commit)
         kDrain,
@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(Cfg<kPacked>::kThreads, 1)
         init(C::kSFull, 2, 1);
         init(C::kSFree, 2, kSetWarps);
         init(C::kRawFull, C::kRawStages, 1);
-        init(C::kRawEmpty, C::kRawStages, 4);
+        init(C::kRawEmpty, C::kRawStages, 8);
         init(C::kKeyFull, 1, 1);
         init(C::kKeyEmpty, 1, 1);
         init(C::kDrain, 1, 1);
@@ -276,8 +276,14 @@ __global__ void __launch_bounds__(Cfg<kPacked>::kThreads, 1)
         walk([&](int j0, int j1, int) {
 #pragma unroll 1
             for (int t = j0; t < j1; ++t, ++n) {
-                const int unit = 2 * n + hi, st = unit % C::kRawStages;
-                if (!wait(C::kRawFull + st, unit / C::kRawStages)) return false;
+                // Every warp waits for both halves of the tile and returns both, though
+                // it reads one: a barrier's parity only tells its phases apart to who
+                // has seen the one before.
+                const int u0 = 2 * n, u1 = 2 * n + 1, st = (u0 + hi) % C::kRawStages;
+                if (!wait(C::kRawFull + u0 % C::kRawStages, u0 / C::kRawStages) ||
+                    !wait(C::kRawFull + u1 % C::kRawStages, u1 / C::kRawStages))
+                    return false;
+                if (lane == 0) mbar_arrive(bar(C::kRawEmpty + (u1 - hi) % C::kRawStages));
                 const uint32_t src = base + C::kOffRaw + st * kRawBytes + (32 * (quarter & 1) + lane) * kRawRow;
                 RawChunk r;
                 r.load(src, odd);
