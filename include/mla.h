@@ -320,8 +320,8 @@ size_t mla_packed_workspace_bytes(const mla_dims_t* dims, int32_t B, int32_t q_l
 /* mla_attend_latent over a packed cache.  lse [B][q_len][H] fp32 (may be
  * NULL) receives the natural log of the sum over keys of exp(s_j), -infinity
  * for a sequence with an invalid length.  Of the options, path, num_pairs,
- * overhead_tiles, min_tiles (both in 128-key tiles here) and wait_limit_ns
- * apply. */
+ * overhead_tiles and min_tiles (both in 128-key tiles here, 1 by default),
+ * wait_limit_ns and withhold_tile apply. */
 int mla_attend_packed(const mla_dims_t* dims, const void* q_hat, const mla_cache_t* cache, const int32_t* seqlens,
                       int32_t B, int32_t q_len, void* o_lat, float* lse, void* workspace, size_t workspace_bytes,
                       const mla_decode_opts_t* opts, mla_stream_t stream);
@@ -359,7 +359,8 @@ int mla_attend_latent_lse(const mla_dims_t* dims, const void* q_hat, const mla_c
  *   weights [B][weights_stride] fp32; entries of rows >= seqlens[b], and of a
  *           sequence with an invalid length (flags MLA_STATUS_BAD_SEQLEN), are left as they were
  * weights_stride >= T_max.  The sums do not depend on how the work is spread (no atomics).
- * Of the options, path and wait_limit_ns apply. */
+ * prev and weights must not overlap otherwise.  Of the options, path,
+ * wait_limit_ns and withhold_tile apply. */
 int mla_accumulate_weights(const mla_dims_t* dims, const void* q_hat, const float* lse, const mla_cache_t* cache,
                            int32_t cache_format, const int32_t* seqlens, int32_t B, int32_t q_len, float decay,
                            const float* prev, float* weights, int64_t weights_stride, const mla_decode_opts_t* opts,

@@ -275,6 +275,9 @@ int mla_accumulate_weights(const mla_dims_t* dims, const void* q_hat, const floa
     if (rc) return rc;
     if (weights_stride < cv.T_max)
         return set_error(MLA_ERR_SHAPE, "weights_stride %lld < cache T_max %d", (long long)weights_stride, cv.T_max);
+    if (prev && prev != weights &&
+        span_of(prev, B, 4 * weights_stride, cv.T_max, 4, 4).overlaps(span_of(weights, B, 4 * weights_stride, cv.T_max, 4, 4)))
+        return set_error(MLA_ERR_ARG, "prev overlaps weights: pass the same array, or one apart from it");
     bool fast;
     rc = choose_path(p, q_len, opts, &fast);
     if (rc) return rc;

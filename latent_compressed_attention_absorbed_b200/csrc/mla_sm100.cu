@@ -386,6 +386,7 @@ cudaError_t sm100_attend_packed(const Problem& p, const void* q_hat, const Cache
     a.lse = lse;
     a.status = status;
     a.wait_limit_ns = (opts && opts->wait_limit_ns > 0) ? (uint64_t)opts->wait_limit_ns : MLA_WAIT_LIMIT_NS;
+    a.withhold_tile = (opts && opts->withhold_tile > 0) ? opts->withhold_tile : -1;
     e = launch_pdl(pk::packed_attend_kernel, dim3(clusters * 2), dim3(pk::kThreads), pk::kSmem, st, 2, mRaw, mRope, a);
     if (e != cudaSuccess) return e;
     if (groups < 2) return cudaSuccess;  // nothing is cut
@@ -445,6 +446,7 @@ cudaError_t sm100_weights(const Problem& p, bool packed, const void* q_hat, cons
     a.T_max = cache.T_max;
     a.status = status;
     a.wait_limit_ns = (opts && opts->wait_limit_ns > 0) ? (uint64_t)opts->wait_limit_ns : MLA_WAIT_LIMIT_NS;
+    a.withhold_tile = (opts && opts->withhold_tile > 0) ? opts->withhold_tile : -1;
     return packed ? weights_launch<true>(mQ, mRows, mKey, a, st) : weights_launch<false>(mQ, mRows, mKey, a, st);
 }
 

@@ -129,6 +129,7 @@ struct Args {
     int cuts_by_seq;
     int* status;
     uint64_t wait_limit_ns;
+    int withhold_tile;           // test hook (>= 0): the loaders stop before this 64-key tile (see mla.h)
 };
 
 // mapRaw: codes and scales [B][T_max][144 x 16 bits], box of whole such rows x 64;
@@ -235,6 +236,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         while (ok && it.next(seq, T, k0, k1, whole)) {
 #pragma unroll 1
             for (int t = 2 * k0; t < 2 * k1; t += per, ++n_load) {
+                if (args.withhold_tile >= 0 && n_load * per >= args.withhold_tile) break;
                 const int st = n_load % kRawStages;
                 if (!wait(empty + st, n_load / kRawStages + 1) || *abort_flag) { ok = false; break; }
                 if (lane == 0) {
@@ -279,7 +281,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int c = 0; c < 8; ++c) {
                     ok = ok && wait(kChFull + c % kChunks, c / kChunks);
                     tc_fence_after();
-                    if (elect_one()) {
+                    if (ok && elect_one()) {
                         const uint64_t dB = dChunk + (((c % kChunks) * kChunkBytes) >> 4);
 #pragma unroll
                         for (int k = 0; k < 4; ++k)

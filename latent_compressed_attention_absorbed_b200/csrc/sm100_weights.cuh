@@ -90,6 +90,7 @@ struct Args {
     int B, q_len, T_max;
     int* status;
     uint64_t wait_limit_ns;
+    int withhold_tile;  // test hook (>= 0): the loader stops before this 64-row tile (see mla.h)
 };
 
 // mapQ: Q-hat [tokens][128 heads][576], box 64 x 128 x 1, SW128.
@@ -169,6 +170,7 @@ __global__ void __launch_bounds__(Cfg<kPacked>::kThreads, 1)
             if constexpr (kPacked) {
 #pragma unroll 1
                 for (int t = 2 * j0; t < 2 * j1; ++t, ++n_load) {
+                    if (args.withhold_tile >= 0 && n_load >= args.withhold_tile) return true;
                     const int st = n_load % C::kRawStages;
                     if (!wait(C::kRawEmpty + st, n_load / C::kRawStages + 1)) return false;
                     if (lane == 0) {
@@ -182,6 +184,7 @@ __global__ void __launch_bounds__(Cfg<kPacked>::kThreads, 1)
                 for (int t = j0; t < j1; ++t)
 #pragma unroll 1
                     for (int c = 0; c < kQChunks; ++c, ++n_load) {
+                        if (args.withhold_tile >= 0 && n_load / kQChunks * 2 + 1 >= args.withhold_tile) return true;
                         const int st = n_load % C::kRing;
                         if (!wait(C::kChEmpty + st, n_load / C::kRing + 1)) return false;
                         if (lane == 0) {

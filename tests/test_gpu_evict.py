@@ -118,6 +118,48 @@ def test_weights_strides_and_repeats(lib):
     assert torch.equal(alone[0], w[0])
 
 
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("T,q_len", [((2000, 700), 1), ((1500,), 3)])
+def test_weights_expired_wait(lib, packed, T, q_len):
+    dims, cache, rows, q, lse, w, before, scale = weights_case(lib, V3, T, q_len, packed)
+    lib.accumulate_weights(dims, q, lse, cache, i32(*T), torch.zeros_like(w),
+                           opts=lib.opts(wait_limit_ns=50_000_000, withhold_tile=1))
+    assert lib.device_status() & 4
+    again = torch.full_like(w, -1.0)
+    lib.accumulate_weights(dims, q, lse, cache, i32(*T), again)
+    assert lib.device_status() == 0 and torch.equal(again, w)
+
+
+@pytest.mark.parametrize("packed", [False, True])
+def test_weights_of_many_short_sequences(lib, packed):
+    # more sequences than a block has threads, some invalid: every valid sequence's weights add up to its queries and heads
+    B, T_max, q_len = 1500, 200, 2
+    dims = dims_of(lib, V3)
+    T = torch.randint(2, T_max + 1, (B,), generator=torch.Generator().manual_seed(4))
+    T[::89] = 1
+    seq = T.to(torch.int32).cuda()
+    q = rand(2, B, q_len, 128, 576, dtype=torch.bfloat16, std=0.05)
+    lse = torch.zeros(B, q_len, 128, device="cuda")
+    if packed:
+        cache = torch.randint(0, 256, (B, T_max, 416), generator=torch.Generator(device="cuda").manual_seed(1), device="cuda", dtype=torch.uint8)
+        cache[:, :, 256:288] = 160
+        cache[:, :, 288:] = torch.randn(B, T_max, 64, device="cuda").bfloat16().view(torch.uint8)
+        lib.attend_packed(dims, q, cache, seq, lse=lse)
+    else:
+        cache = rand(3, B, T_max, 576, dtype=torch.bfloat16)
+        lib.attend_latent_lse(dims, q, cache, seq, lse)
+    w = torch.zeros(B, T_max, device="cuda")
+    lib.accumulate_weights(dims, q, lse, cache, seq, w)
+    assert lib.device_status() == 2
+    # each of 256 terms of a sequence's total carries the score's and the exponential's rounding, below 1e-4
+    want = torch.where(T.cuda() < q_len, 0.0, 256.0)
+    assert torch.all((w.sum(1) - want).abs() <= 256 * 1e-4)
+    v = torch.zeros(B, T_max, device="cuda")
+    lib.accumulate_weights(dims, q, lse, cache, seq, v, opts=lib.opts(path=2))
+    assert lib.device_status() == 2
+    assert torch.all((w - v).abs() <= 2e-4 * v + 1e-6)
+
+
 # ------------------------------------------------------------------ evict
 
 def evict_case(lib, g, T, budget, sink, recent, packed=False, T_max=None, in_place=False, w=None, seed=4, strided=False):
@@ -204,6 +246,17 @@ def test_evict_weights_of_every_kind(lib, T):
         evict_case(lib, TINY, (T,), budget, 2, 30, w=w.clone(), in_place=True)
     for value in (0.0, float("nan"), 7.0):
         evict_case(lib, TINY, (T,), T // 2, 2, 30, w=torch.full((1, T), value, device="cuda"), in_place=True)
+
+
+def test_evict_beyond_one_slab(lib):
+    # more rows than the selection's registers hold (131072), in and out of place, next to a short sequence
+    for in_place in (False, True):
+        evict_case(lib, TINY, (300000, 140001, 500), 100000, 16, 1000, in_place=in_place)
+
+
+def test_evict_many_sequences(lib):
+    T = torch.randint(0, 300, (1500,), generator=torch.Generator().manual_seed(5)).tolist()
+    evict_case(lib, TINY, tuple(T), 100, 4, 20, T_max=299, in_place=True)
 
 
 def test_evict_long_in_place(lib):

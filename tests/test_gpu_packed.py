@@ -422,3 +422,77 @@ def test_cache_of_more_than_two_to_the_31_bytes(lib):
     assert lib.device_status() == 0
     assert torch.equal(o[8:], lib.attend_packed(dims, q[8:], small, i32(300), opts=one))
     assert torch.equal(lib.load_packed(dims, cache, i32(*([0] * 8 + [T_max - 1])), 1)[8:], lib.load_packed(dims, small, i32(299), 1))
+
+
+# ------------------------------------------------------------------ edges of the calls
+
+def test_many_short_sequences(lib):
+    # more sequences than threads of a block plan for, some of them invalid, against the CUDA-core path
+    B, T_max, q_len = 1500, 300, 2
+    dims = dims_of(lib, V3)
+    g = torch.Generator().manual_seed(3)
+    T = torch.randint(2, T_max + 1, (B,), generator=g)
+    T[::97] = 1                                   # shorter than the queries
+    T[5] = T_max + 1
+    cache = torch.randint(0, 256, (B, T_max, 416), generator=torch.Generator(device="cuda").manual_seed(1), device="cuda", dtype=torch.uint8)
+    cache[:, :, 256:288] = 160                    # every scale 1/2, so that the values are of one size
+    cache[:, :, 288:] = torch.randn(B, T_max, 64, device="cuda").bfloat16().view(torch.uint8)
+    q = rand(2, B, q_len, 128, 576, dtype=torch.bfloat16, std=0.05)
+    seq = T.to(torch.int32).cuda()
+    out = {}
+    for path in (0, 2):
+        lse = torch.zeros(B, q_len, 128, device="cuda")
+        o = lib.attend_packed(dims, q, cache, seq, lse=lse, opts=lib.opts(path=path))
+        assert lib.device_status() == 2
+        out[path] = (o.float(), lse)
+    bad = (T < q_len) | (T > T_max)
+    assert not out[0][0][bad].any() and torch.all(out[0][1][bad] == -float("inf"))
+    good = (~bad).cuda()
+    # both paths round the output once (2^-8 each) and hold the weights to 2^-11
+    a, b = out[0][0][good], out[2][0][good]
+    assert torch.all((a - b).abs() <= 2.0 ** -7 * b.abs() + 2.0 ** -9 * 4)   # |latents| <= 4
+    assert torch.all((out[0][1][good] - out[2][1][good]).abs() <= 1e-4)
+
+
+def test_sixteen_byte_alignment_is_enough(lib):
+    T = (300, 77)
+    dims, cache, rows, q, o, lse = attend_case(lib, V3, T, 2)
+
+    def off(t):  # the same tensor 16 bytes into a buffer
+        n = t.numel() * t.element_size()
+        buf = torch.zeros(n + 32, dtype=torch.uint8, device="cuda")
+        at = 16 if buf.data_ptr() % 32 == 0 else 0
+        v = buf[at:at + n].view(t.dtype).view(t.shape)
+        v.copy_(t)
+        return v
+    o2 = off(torch.zeros_like(o))
+    ws = torch.empty(lib.packed_workspace_bytes(dims, 2, 2) + 16, dtype=torch.uint8, device="cuda")[16:]
+    lib.attend_packed(dims, off(q), off(cache), off(i32(*T)), out=o2, workspace=ws)
+    assert lib.device_status() == 0 and torch.equal(o, o2)
+
+
+def test_empty_calls(lib):
+    dims = dims_of(lib, V3)
+    e = torch.empty
+    u8, bf = dict(dtype=torch.uint8, device="cuda"), dict(dtype=torch.bfloat16, device="cuda")
+    none = i32()
+    cache = torch.zeros(2, 8, 416, **u8)
+    lib.append_packed(dims, cache, e(0, 1, 512, **bf), e(0, 1, 64, **bf), none)
+    lib.append_packed(dims, cache, e(2, 0, 512, **bf), e(2, 0, 64, **bf), i32(0, 0))
+    assert lib.load_packed(dims, cache, none, 3).shape == (0, 3, 576)
+    assert lib.attend_packed(dims, e(0, 1, 128, 576, **bf), cache, none).shape == (0, 1, 128, 512)
+    lib.accumulate_weights(dims, e(0, 1, 128, 576, **bf), e(0, 1, 128, device="cuda"), cache, none, e(0, 8, device="cuda"))
+    lib.evict(dims, cache, e(0, 8, device="cuda"), none, 4)
+    assert lib.device_status() == 0 and not cache.any()
+
+
+@pytest.mark.parametrize("T,q_len,pairs", [((700, 333, 64), 1, 2), ((900, 77), 2, 4), ((5000,), 1, 1)])
+def test_expired_wait(lib, T, q_len, pairs):
+    # the loaders stop before the third 64-key tile, so that a bounded wait runs out (50 ms); the kernel reports it, ends in
+    # order, and the next call is right
+    from latent_compressed_attention_absorbed_b200 import binding
+    dims, cache, rows, q, o, lse = attend_case(lib, V3, T, q_len, lib.opts(num_pairs=pairs))
+    lib.attend_packed(dims, q, cache, i32(*T), opts=lib.opts(num_pairs=pairs, wait_limit_ns=50_000_000, withhold_tile=3))
+    assert lib.device_status() & binding.STATUS_TIMEOUT
+    assert torch.equal(lib.attend_packed(dims, q, cache, i32(*T), opts=lib.opts(num_pairs=pairs)), o)
+    assert lib.device_status() == 0

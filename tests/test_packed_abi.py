@@ -114,6 +114,7 @@ def test_weights_refusals(L, mem):
     assert weights(q=None) == ARG and weights(lse=None) == ARG and weights(w=None) == ARG and weights(s=None) == ARG
     assert weights(w=bad) == ALIGN and weights(prev=bad) == ALIGN and weights(lse=bad) == ALIGN
     assert weights(B=0, q=None) == 0
+    assert weights(prev=ctypes.c_void_p(a + 4)) == ARG               # overlaps weights, one entry on
 
 
 def test_evict_refusals(L, mem):
