@@ -83,7 +83,7 @@ __global__ void append_v3_kernel(const __nv_bfloat16* __restrict__ c_kv, const _
     MLA_KT(kKtAppend, 2);
 }
 
-bool g_smem_absorb[kMaxDev], g_smem_project[kMaxDev], g_smem_attend[kMaxDev], g_smem_packed[kMaxDev];
+bool g_smem_absorb[kMaxDev], g_smem_project[kMaxDev], g_smem_attend[2][kMaxDev], g_smem_packed[kMaxDev];
 bool g_smem_weights[2][kMaxDev];
 bool g_smem_absorb_gemv[4][kMaxDev], g_smem_project_gemv[4][kMaxDev];
 
@@ -303,13 +303,14 @@ cudaError_t sm100_attend(const Problem& p, const void* q_hat, const CacheView& c
 
     cudaError_t e;
     if (!plan_ready) {
-        mla_plan_kernel<kNk><<<1, 32, 0, st>>>(seqlens, p.B, p.q_len, cache.T_max, clusters, plan_ovh(overhead_tiles),
+        mla_plan_kernel<<<1, 32, 0, st>>>(seqlens, p.B, p.q_len, cache.T_max, clusters, plan_ovh(overhead_tiles),
                                           plan_min_units(min_tiles), plan, status, (__nv_bfloat16*)o_lat, lse);
         e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
 
-    e = set_smem(mla_attend_kernel, kAttSmem, g_smem_attend);
+    const auto attend = lse ? mla_attend_kernel<true> : mla_attend_kernel<false>;
+    e = set_smem(attend, kAttSmem, g_smem_attend[lse != nullptr]);
     if (e != cudaSuccess) return e;
     AttendArgs a;
     a.plan = plan;
@@ -333,7 +334,7 @@ cudaError_t sm100_attend(const Problem& p, const void* q_hat, const CacheView& c
     a.T_max = cache.T_max;
 
     if (events) events->record(MLA_EV_ATTEND_BEGIN, st);
-    e = launch_pdl(mla_attend_kernel, dim3(clusters * 2), dim3(kAttThreads), kAttSmem, st, 2, mRow, a);
+    e = launch_pdl(attend, dim3(clusters * 2), dim3(kAttThreads), kAttSmem, st, 2, mRow, a);
     if (e != cudaSuccess) return e;
     if (events) events->record(MLA_EV_ATTEND_END, st);
 

@@ -357,6 +357,11 @@ __device__ __forceinline__ void zero_rows(uint32_t tile, int nchunks, int r0, in
 }
 
 // mapRow: the cache [B][T_max][576] bf16, box 64 columns x 64 keys, SW128.
+// kLse: the rows' LSE is asked for.  (A form of its own, because the kernel's
+// time hangs on how its code lies in the instruction cache: with one form that
+// tested the pointer, 8 x 131072 rows took 473 us where the form without takes
+// 393; the stores below in a form of their own, 396 to 399.)
+template <bool kLse>
 __global__ void __launch_bounds__(kAttThreads, 1)
     mla_attend_kernel(const __grid_constant__ CUtensorMap mapRow, AttendArgs args) {
     extern __shared__ uint8_t smem_raw[];
@@ -726,13 +731,17 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                 rl[kh * kHeads + m] = l_part;
                 named_bar_sync(1 + quarter, 64);
                 const float l_sum = rl[m] + rl[kHeads + m];
-                if (ok && kh == 0 && (!w.whole || args.lse)) {
-                    if (w.whole) {
-                        args.lse[((size_t)w.seq * q_len + qi) * kHeads + m] = lse_natural(m_used, l_sum);
-                    } else {
-                        const size_t pslot = (size_t)(grp + w.seq) * q_len + qi;
-                        args.part_lse[pslot * kHeads + m] = l_sum > 0.f ? m_used + __log2f(l_sum) : -CUDART_INF_F;
+                if constexpr (kLse) {
+                    // (base 2 for the merge, natural for the caller)
+                    float* const dst = w.whole ? args.lse : args.part_lse;
+                    if (ok && kh == 0) {
+                        const size_t row = (size_t)(w.whole ? w.seq : grp + w.seq) * q_len + qi;
+                        const float v = l_sum > 0.f ? m_used + __log2f(l_sum) : -CUDART_INF_F;
+                        dst[row * kHeads + m] = w.whole ? v * 0.6931471805599453f : v;
                     }
+                } else if (ok && !w.whole && kh == 0) {
+                    const size_t pslot = (size_t)(grp + w.seq) * q_len + qi;
+                    args.part_lse[pslot * kHeads + m] = l_sum > 0.f ? m_used + __log2f(l_sum) : -CUDART_INF_F;
                 }
                 m_used = -CUDART_INF_F;
                 l_part = 0.f;
@@ -951,12 +960,11 @@ __global__ void __launch_bounds__(kAttThreads, 1)
 
 // ------------------------------------------------------------------ plan
 
-// Per sequence: cost_b = ceil(T_b / kTile) + ovh (0 for an invalid length);
+// Per sequence: cost_b = ceil(T_b / 64) + ovh (0 for an invalid length);
 // prefix sums, the per-group share L = ceil(total / groups) (at least
 // min_units), the list of sequences cut across groups, and o_lat = 0 for the
 // tokens of sequences with an invalid length (their decode has no defined
 // result).  One warp.
-template <int kTile = kNk>
 __device__ __forceinline__ void mla_plan_warp(const int32_t* __restrict__ seqlens, int B, int q_len, int T_max,
                                               int clusters, int ovh, int min_units, Plan* plan, int* status,
                                               __nv_bfloat16* o_lat, int lane) {
@@ -973,7 +981,7 @@ __device__ __forceinline__ void mla_plan_warp(const int32_t* __restrict__ seqlen
         if (b < B) {
             const int T = seqlens[b];
             if (T < q_len || T > T_max) atomicOr(status, MLA_STATUS_BAD_SEQLEN);
-            else c = (T + kTile - 1) / kTile + ovh;
+            else c = (T + kNk - 1) / kNk + ovh;
             c_min = min(c_min, c);
             c_max = max(c_max, c);
         }
@@ -1037,11 +1045,10 @@ __device__ __forceinline__ void mla_plan_warp(const int32_t* __restrict__ seqlen
     }
 }
 
-template <int kTile>
 __global__ void __launch_bounds__(32) mla_plan_kernel(const int32_t* __restrict__ seqlens, int B, int q_len,
                                                       int T_max, int clusters, int ovh, int min_units, Plan* plan,
                                                       int* status, __nv_bfloat16* o_lat, float* lse) {
-    mla_plan_warp<kTile>(seqlens, B, q_len, T_max, clusters, ovh, min_units, plan, status, o_lat, threadIdx.x);
+    mla_plan_warp(seqlens, B, q_len, T_max, clusters, ovh, min_units, plan, status, o_lat, threadIdx.x);
     if (!lse) return;
     for (int b = 0; b < B; ++b) {
         const int T = seqlens[b];
