@@ -297,9 +297,12 @@ static int evict_row_bytes(const Problem& p, int format) {
                                       : (p.d_c + p.d_r) * (int)elem_size(p);
 }
 
+// Rows and chunks of rows are counted in 32 bits, with room to run past the budget by a block's threads.
+static constexpr int32_t kMaxBudget = 1 << 30;
+
 size_t mla_evict_workspace_bytes(const mla_dims_t* dims, int32_t cache_format, int32_t B, int32_t budget) {
     Problem p;
-    if (check_dims(dims, &p) || B < 0 || budget < 1) return 0;
+    if (check_dims(dims, &p) || B < 0 || budget < 1 || budget > kMaxBudget) return 0;
     if (cache_format != MLA_CACHE_FULL && cache_format != MLA_CACHE_PACKED) return 0;
     if (cache_format == MLA_CACHE_PACKED && check_packed_dims(p)) return 0;
     return evict_workspace(B, budget, evict_row_bytes(p, cache_format)) + kWsAlign;
@@ -313,7 +316,8 @@ int mla_evict(const mla_dims_t* dims, const mla_cache_t* cache, int32_t cache_fo
     Problem p;
     int rc = check_dims(dims, &p);
     if (rc) return rc;
-    if (B < 0 || budget < 1) return set_error(MLA_ERR_ARG, "need B >= 0 and budget >= 1");
+    if (B < 0 || budget < 1 || budget > kMaxBudget)
+        return set_error(MLA_ERR_ARG, "need B >= 0 and 1 <= budget <= %d", kMaxBudget);
     if (n_sink < 0 || n_recent < 0 || (int64_t)n_sink + n_recent > budget)
         return set_error(MLA_ERR_ARG, "need n_sink >= 0, n_recent >= 0 and n_sink + n_recent <= budget (%d + %d, %d)", n_sink,
                          n_recent, budget);
@@ -362,6 +366,8 @@ int mla_evict(const mla_dims_t* dims, const mla_cache_t* cache, int32_t cache_fo
                      : span_of(weights, B, 4 * weights_stride, from.T_max, 4, 4)
                            .overlaps(span_of(out_weights, B, 4 * out_weights_stride, most, 4, 4)))
         return set_error(MLA_ERR_ARG, "out_weights overlaps weights: pass the same array, or one apart from it");
+    if (seqlens != out_seqlens && span_of(seqlens, 1, 0, B, 4, 4).overlaps(span_of(out_seqlens, 1, 0, B, 4, 4)))
+        return set_error(MLA_ERR_ARG, "out_seqlens overlaps seqlens: pass the same array, or one apart from it");
     a.in_place = rows_same || weights_same;
     const size_t need = evict_workspace(B, budget, a.row_bytes) + kWsAlign;
     if (!workspace || workspace_bytes < need || !aligned16(workspace))

@@ -145,6 +145,24 @@ def test_evict_refusals(L, mem):
     assert evict(ws=None) == WORKSPACE and evict(nbytes=16) == WORKSPACE
 
 
+def test_eviction_of_seqlens_shifted_and_of_budgets_past_32_bits(L, mem):
+    _, a = mem
+    d, p = ctypes.byref(TINY), ctypes.c_void_p(a)
+    src, dst = bd.Cache(a, 2, 8, 8 * 40, 40), bd.Cache(a + 4096, 2, 8, 8 * 40, 40)
+    w, wo = ctypes.c_void_p(a + 8192), ctypes.c_void_p(a + 12288)
+
+    def evict(s, n, budget=4):
+        return L.mla_evict(d, ctypes.byref(src), 0, w, 8, s, 2, budget, 1, 1, ctypes.byref(dst), wo, 8, n, None, p, 16, None)
+
+    assert evict(p, ctypes.c_void_p(a + 4)) == ARG and evict(ctypes.c_void_p(a + 4), p) == ARG  # a sequence's length under another's
+    assert evict(p, p) == WORKSPACE and evict(p, ctypes.c_void_p(a + 8)) == WORKSPACE           # (16 bytes are too few)
+    for budget in (2**30 + 1, 2**31 - 1):  # counting the chunks of such a budget would wrap
+        assert evict(p, p, budget=budget) == ARG
+        assert L.mla_evict_workspace_bytes(d, 0, 2, budget) == 0
+    assert evict(p, p, budget=2**30) == WORKSPACE
+    assert L.mla_evict_workspace_bytes(d, 0, 2, 2**30) >= 2 * 2**30 * 4
+
+
 def test_binding_refuses_wrong_tensors():
     # every check comes before the library is called, on the CPU
     lib = bd.Library()
