@@ -150,6 +150,15 @@ def _need_weights(t, name, device, B):
         raise ValueError(f"{name} is on {t.device}, the other tensors on {device}")
 
 
+def _empty(shape, dtype, device, stream) -> torch.Tensor:
+    """A new tensor for a call on ``stream``: allocated there, as memory that the allocator hands out for the current
+    stream may still be in use on it, and may be handed out again there before ``stream`` has got to the call."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 class Library:
     def __init__(self, path: str = LIB_PATH):
         if not os.path.exists(path):
@@ -399,7 +408,7 @@ class Library:
         B = rows.shape[0]
         shape = (B, n_tok, dims.d_c + dims.d_r)
         if out is None:
-            out = torch.empty(shape, dtype=dt, device=dev)
+            out = _empty(shape, dt, dev, stream)
         else:
             _expect(out, "out", dt, shape, dev)
         self._call(self.lib.mla_load_packed, dev, stream, dims, cd, rows.data_ptr(), B, n_tok, out.data_ptr())
@@ -409,12 +418,12 @@ class Library:
         return int(self.lib.mla_packed_workspace_bytes(ctypes.byref(dims), B, q_len))
 
     @staticmethod
-    def _scratch(workspace, nbytes, device):
+    def _scratch(workspace, nbytes, device, stream):
         """The caller's workspace, or a new one of nbytes() bytes."""
         if workspace is None:
             with torch.cuda.device(device):  # (the size depends on the device)
                 n = nbytes()
-            return torch.empty(max(n, 16), dtype=torch.uint8, device=device)
+            return _empty(max(n, 16), torch.uint8, device, stream)
         _need(workspace, "workspace", dtype=torch.uint8)
         if workspace.device != device:
             raise ValueError(f"workspace is on {workspace.device}, the other tensors on {device}")
@@ -430,10 +439,10 @@ class Library:
         _expect(lse, "lse", torch.float32, (B, q_len, dims.H), dev)
         shape = (B, q_len, dims.H, dims.d_c)
         if out is None:
-            out = torch.empty(shape, dtype=dt, device=dev)
+            out = _empty(shape, dt, dev, stream)
         else:
             _expect(out, "out", dt, shape, dev)
-        ws = self._scratch(workspace, lambda: size(dims, B, q_len), dev)
+        ws = self._scratch(workspace, lambda: size(dims, B, q_len), dev, stream)
         self._call(fn, dev, stream, dims, q_hat.data_ptr(), cd, seqlens.data_ptr(), B, q_len, out.data_ptr(),
                    None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.numel(), opts)
         return out
@@ -462,10 +471,10 @@ class Library:
         _expect(lse, "lse", torch.float32, (B, q_len, dims.H), dev)
         shape = (B, q_len, dims.H, dims.d_v)
         if out is None:
-            out = torch.empty(shape, dtype=dt, device=dev)
+            out = _empty(shape, dt, dev, stream)
         else:
             _expect(out, "out", dt, shape, dev)
-        ws = self._scratch(workspace, lambda: self.packed_workspace_bytes(dims, B, q_len), dev)
+        ws = self._scratch(workspace, lambda: self.packed_workspace_bytes(dims, B, q_len), dev, stream)
         self._call(self.lib.mla_decode_packed, dev, stream, dims, q_nope.data_ptr(), q_rope.data_ptr(), W_UK.data_ptr(),
                    W_UV.data_ptr(), cd, seqlens.data_ptr(), None if n_seen is None else n_seen.data_ptr(), B, q_len,
                    out.data_ptr(), None if q_hat is None else q_hat.data_ptr(), None if lse is None else lse.data_ptr(),
@@ -534,7 +543,8 @@ class Library:
         else:
             _expect(out_seqlens, "out_seqlens", torch.int32, (B,), dev)
         _expect(kept, "kept", torch.int32, (B, budget), dev)
-        ws = self._scratch(workspace, lambda: self.evict_workspace_bytes(dims, B, budget, fmt == CACHE_PACKED), dev)
+        ws = self._scratch(workspace, lambda: self.evict_workspace_bytes(dims, B, budget, fmt == CACHE_PACKED), dev,
+                           stream)
         self._call(self.lib.mla_evict, dev, stream, dims, cd, fmt, weights.data_ptr(), sw, seqlens.data_ptr(), B, budget,
                    n_sink, n_recent, od, out_weights.data_ptr(), so, out_seqlens.data_ptr(),
                    None if kept is None else kept.data_ptr(), ws.data_ptr(), ws.numel())

@@ -13,7 +13,6 @@ namespace sm100 {
 constexpr int kPackNib = 256;    // bytes of codes of a V3 row
 constexpr int kPackScale = 32;   // bytes of scales
 constexpr int kPackRope = 288;   // where its key starts
-constexpr int kPackRow = 416;
 
 __device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
     uint32_t r;

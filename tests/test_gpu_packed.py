@@ -496,3 +496,34 @@ def test_expired_wait(lib, T, q_len, pairs):
     assert lib.device_status() & binding.STATUS_TIMEOUT
     assert torch.equal(lib.attend_packed(dims, q, cache, i32(*T), opts=lib.opts(num_pairs=pairs)), o)
     assert lib.device_status() == 0
+
+
+def test_new_memory_belongs_to_the_calls_stream(lib, monkeypatch):
+    # memory of the current stream may still be in use there, and would be handed out again there too early
+    T = (300, 40)
+    dims = dims_of(lib, V3)
+    cache, _ = make_cache(lib, dims, V3, T)
+    full = rand(3, 2, 300, 576, dtype=torch.bfloat16)
+    ins = decode_inputs(V3, 2, 1)
+    q = rand(2, 2, 1, 128, 576, dtype=torch.bfloat16, std=0.25)
+    seq, first, lse, w = i32(*T), i32(0, 0), torch.zeros(2, 1, 128, device="cuda"), rand(4, 2, 300)
+    calls = (lambda s: lib.attend_packed(dims, q, cache, seq, stream=s),
+             lambda s: lib.decode_packed(dims, *ins, cache, seq, stream=s),
+             lambda s: lib.load_packed(dims, cache, first, 40, stream=s),
+             lambda s: lib.attend_latent_lse(dims, q, full, seq, lse, stream=s))
+    ref = [call(None) for call in calls]
+    used, empty = [], torch.empty
+
+    def recorded(*a, **k):
+        used.append(torch.cuda.current_stream())
+        return empty(*a, **k)
+
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    monkeypatch.setattr(torch, "empty", recorded)
+    got = [call(s) for call in calls]
+    lib.evict(dims, cache, w, seq, 100, stream=s)
+    s.synchronize()
+    assert used and all(u == s for u in used)
+    assert all(torch.equal(a, b) for a, b in zip(got, ref))
+    assert seq.tolist() == [100, 40] and lib.device_status() == 0
