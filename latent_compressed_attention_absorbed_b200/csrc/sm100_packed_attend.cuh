@@ -96,7 +96,7 @@ enum {
     kRopeEmpty,                        // keys multiplied (MMA commit)
     kSFull,                            // S(g) complete (MMA commit)
     kSFree = kSFull + 2,               // S buffer read (8 warps)
-    kQFull = kSFree + 2,               // Q-hat of a piece in place (4 warps)
+    kQFull = kSFree + 2,               // Q-hat of a piece in place (8 warps)
     kQRead,                            // last S of a piece complete
     kSlotFree,                         // accumulator's P slot consumed (remote)
     // accumulator
@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             init(kRopeEmpty, 1, 1);
             init(kSFull, 2, 1);
             init(kSFree, 2, 8);
-            init(kQFull, 1, 4);
+            init(kQFull, 1, 8);
             init(kQRead, 1, 1);
             init(kSlotFree, kSlots, 1);
         } else {
@@ -305,71 +305,71 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (rank == 0 && ((warp >= 6 && warp <= 11) || warp == 16 || warp == 17)) {
         // ======================================================== scorer: unpacking warps, a row of the tile a lane
         // Two sets of four warps take the even (10, 11, 16, 17) and the odd chunks
-        // (6-9).  The second set first loads a piece's Q-hat: row m's 512 latent
-        // values -> TMEM columns 0..255, read coalesced and transposed through the
-        // RoPE part's own buffer, where the last block, the RoPE part, stays as
-        // the shared-memory operand.
-        const bool loader = warp <= 9;
-        const int odd = loader ? 1 : 0;
-        const int row = 32 * (loader ? quarter : (warp < 12 ? warp - 10 : warp - 14)) + lane;
+        // (6-9).  First they share a piece's Q-hat out in the same way: row m's 512
+        // latent values -> TMEM columns 0..255, 64 values in turn, read coalesced
+        // and transposed through the first set's own first chunk and the RoPE
+        // part's buffer, where the second set's last block, the RoPE part, stays
+        // as the shared-memory operand.
+        const int odd = warp <= 9 ? 1 : 0;
+        const int row = 32 * quarter + lane;
         const uint32_t row_at = base + kOffChunk + sw128(row, 0);
+        const uint32_t qbuf = base + (odd ? kOffQ : kOffChunk) + quarter * 32 * 128;
+        const int rr = lane >> 3, pc = lane & 7;
         int g = 0;
         for (int seg = 0; ok && it.next(seq, T, k0, k1, whole); ++seg) {
-            if (loader) {
-                // the last S of the previous piece has read Q-hat
-                if (!wait(kQRead, seg + 1) || *abort_flag) { ok = false; break; }
-                tc_fence_after();
-                const uint32_t qbuf = base + kOffQ + quarter * 32 * 128;
-                const int rr = lane >> 3, pc = lane & 7;
-                const int u = seq * q_len + qi;
-                const uint4* src = reinterpret_cast<const uint4*>(args.q_hat + ((size_t)u * kHeads + quarter * 32 + rr) * kRow) + pc;
-                uint4 cur[8], nxt[8];
+            const int u = seq * q_len + qi;
+            const uint4* src = reinterpret_cast<const uint4*>(args.q_hat + ((size_t)u * kHeads + quarter * 32 + rr) * kRow) + pc;
+            uint4 cur[8], nxt[8];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) cur[j] = __ldg(src + (size_t)(4 * j) * (kRow / 8));
+            for (int j = 0; j < 8; ++j) cur[j] = __ldg(src + (size_t)(4 * j) * (kRow / 8) + 8 * odd);
+            // the last S of the previous piece has read Q-hat and the chunks
+            if (!wait(kQRead, seg + 1) || *abort_flag) { ok = false; break; }
+            tc_fence_after();
 #pragma unroll 1
-                for (int c = 0; c < 9; ++c) {
-                    if (c + 1 < 9) {
+            for (int i = 0; i < 4 + odd; ++i) {
+                const int c = i < 4 ? 2 * i + odd : 8;
+                if (i + 1 < 4 + odd) {
+                    const int next = i + 1 < 4 ? c + 2 : 8;
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) nxt[j] = __ldg(src + (size_t)(4 * j) * (kRow / 8) + 8 * (c + 1));
-                    }
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const int r = 4 * j + rr;
-                        st_shared_v4(qbuf + sw128(r, pc), cur[j].x, cur[j].y, cur[j].z, cur[j].w);
-                    }
-                    __syncwarp();
-                    if (c == 8) break;
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        uint32_t v[16];
-#pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            ld_shared_v4u(qbuf + sw128(lane, 4 * h + q), v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
-                        tmem_st16(tmem + lane_addr + kTmemQ + 32 * c + 16 * h, v);
-                    }
-                    __syncwarp();
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) cur[j] = nxt[j];
+                    for (int j = 0; j < 8; ++j) nxt[j] = __ldg(src + (size_t)(4 * j) * (kRow / 8) + 8 * next);
                 }
-                tmem_wait_st();
-                fence_proxy_async_smem();
-                tc_fence_before();
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int r = 4 * j + rr;
+                    st_shared_v4(qbuf + sw128(r, pc), cur[j].x, cur[j].y, cur[j].z, cur[j].w);
+                }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar(kQFull));
+                if (c == 8) break;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t v[16];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        ld_shared_v4u(qbuf + sw128(lane, 4 * h + q), v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+                    tmem_st16(tmem + lane_addr + kTmemQ + 32 * c + 16 * h, v);
+                }
+                __syncwarp();
+#pragma unroll
+                for (int j = 0; j < 8; ++j) cur[j] = nxt[j];
             }
+            tmem_wait_st();
+            fence_proxy_async_smem();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(kQFull));
 #pragma unroll 1
             for (int t = k0; t < k1 && ok; ++t, ++g) {
                 const int st = g % kRawStages;
                 if (!wait(kRawFull + st, g / kRawStages) || *abort_flag) { ok = false; break; }
-                const uint32_t src = base + st * kRawBytes + row * kRawRow;
+                const uint32_t raw_row = base + st * kRawBytes + row * kRawRow;
                 RawChunk raw;
-                raw.load(src, odd);
+                raw.load(raw_row, odd);
 #pragma unroll 1
                 for (int c = odd; c < 8; c += 2) {
                     const int slot = c % kChunks;
                     if (!wait(kChEmpty + slot, c / kChunks + 1)) { ok = false; break; }
                     raw.unpack<false>(row_at + slot * kChunkBytes);
-                    if (c + 2 < 8) raw.load(src, c + 2);
+                    if (c + 2 < 8) raw.load(raw_row, c + 2);
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) {
