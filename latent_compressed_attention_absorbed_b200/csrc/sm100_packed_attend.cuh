@@ -19,7 +19,7 @@
 //     part is the shared-memory A operand of the last four products.
 //   * Unpacked latents stream through a ring of four chunks of 128 keys x 64
 //     latents (bf16: the scores' A operand is bf16 and both operands have one
-//     type); four warps unpack a row each, 11 instructions for 8 values.
+//     type); two sets of four warps unpack alternate chunks, a lane a row.
 //   * P goes to the accumulator in units of 64 keys as fp16, scaled by 2^7, and
 //     the accumulator unpacks the latents to fp16: every value is exact in
 //     either type, and P keeps 11 bits where bf16 keeps 8.  P is at most 2^15
@@ -29,9 +29,20 @@
 //     sequence's end need no clearing: their scores are replaced by -infinity
 //     (a NaN key only reaches its own score), and 0 times a finite number is 0.
 //
+// Measured (B200, 128 heads; bursts of twenty calls, and in brackets calls in a
+// row for seconds): 1 x 4096 rows 28 us, most of it the latency of one tile and
+// of the merge; 64 x 4096 rows 104 us; 8 x 131072 rows 307 (348) us, 950 (840)
+// TFLOP/s; 128 x 2048..16384 rows with two queries 684 (780) us, 990 (870).  What holds the
+// long ones up is power: at 993 W the clock falls to 1.75 GHz, and fewer
+// instructions a value gained 5 % where deeper rings, other bank layouts and
+// earlier hand-offs, which only hide latency, gained nothing.  Code counts too:
+// inline waits whose spin loops did not fit the instruction cache, and an
+// issuing branch that the compiler did not know to be uniform (lane == 0), cost
+// a fifth each.
+//
 // Roles (640 threads; warp w reaches TMEM lanes 32*(w%4)..+31):
 //   scorer:      warp 0 producer of packed rows; 1 TMEM owner and S issuer; 2-5 and 12-15 softmax (two per TMEM quarter,
-//                64 keys each); 10, 11, 16, 17 unpack even chunks; 6-9 load Q-hat once a piece and unpack odd chunks;
+//                64 keys each); 10, 11, 16, 17 unpack even chunks; 6-9 odd chunks, and both sets load a piece's Q-hat;
 //                18 producer of keys
 //   accumulator: warp 0 producer of packed rows; 1 TMEM owner and O issuer; 2-5 and 12-15 rescale / epilogue (two per
 //                quarter, 256 columns each); 6-9 and 16-19 unpack; 10 returns consumed P slots; 11 notes the cuts
@@ -89,7 +100,7 @@ constexpr float kPShift = 7.0f;
 enum {
     // scorer
     kRawFull = 0,                      // packed rows loaded (tx)
-    kRawEmpty = kRawFull + kRawStages, // read by the four unpacking warps
+    kRawEmpty = kRawFull + kRawStages, // read by the eight unpacking warps
     kChFull = kRawEmpty + kRawStages,  // chunk unpacked (4 warps)
     kChEmpty = kChFull + kChunks,      // chunk multiplied (MMA commit)
     kRopeFull = kChEmpty + kChunks,    // keys loaded (tx)
@@ -102,7 +113,7 @@ enum {
     // accumulator
     kARawFull = kSlotFree + kSlots,
     kARawEmpty = kARawFull + kARawStages,
-    kVFull = kARawEmpty + kARawStages,  // unit unpacked (4 warps)
+    kVFull = kARawEmpty + kARawStages,  // unit unpacked (8 warps)
     kVEmpty = kVFull + kVStages,        // unit multiplied (MMA commit)
     kPFull = kVEmpty + kVStages,        // P of a unit landed (tx)
     kPDone = kPFull + kSlots,           // O of a unit complete (MMA commit)
