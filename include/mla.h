@@ -376,7 +376,8 @@ int mla_accumulate_weights(const mla_dims_t* dims, const void* q_hat, const floa
  * out_cache may be the cache itself, out_weights weights, out_seqlens seqlens
  * (eviction in place); other overlaps of these pairs are refused, and so is a
  * budget above 2^30.  Rows of out_cache and entries of
- * out_weights past the kept ones are left as they were.  A sequence with a
+ * out_weights past the kept ones are left as they were: before such a row is
+ * appended to again, the caller sets its weight to zero.  A sequence with a
  * negative length or one above T_max keeps nothing and flags
  * MLA_STATUS_BAD_SEQLEN.  The workspace is of mla_evict_workspace_bytes()
  * bytes, 16-byte aligned, the call's until the stream reaches its end. */
