@@ -25,8 +25,8 @@
 // Measured (B200, bursts): 1 x 4096 full-width rows 11 us (two thirds of it the
 // launch, Q-hat's load and the end); 8 x 65536..131072 rows 187 us, 5.1 TB/s, 0.79
 // of the copy's bandwidth (the power limit is reached there, with the clock at
-// 1.24 GHz); 64 x 2048..16384 packed rows with two queries 218 us, 0.48 of the
-// products' rate, bound by the unpacking warps' instructions.
+// 1.24 GHz); 64 x 2048..16384 packed rows with two queries 157 us, 0.67 of the
+// products' rate.
 //
 // Every wait is bounded; no warp waits on a barrier without a limit before
 // the common end, so a wait that expires ends the kernel in order.
@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(Cfg<kPacked>::kThreads, 1)
         const uint64_t dQ = smem_desc(base, 16, 1024, kSw128);
         const uint64_t dRing = smem_desc(base + C::kOffRing, 16, 1024, kSw128);
         int used[2] = {0, 0};  // tiles each set has been given
-        int n = 0;             // ring chunks multiplied
+        int n = 0;             // full width: ring chunks multiplied; packed: tiles
         walk([&](int j0, int j1, int) {
 #pragma unroll 1
             for (int t = j0; t < j1; ++t) {
@@ -245,37 +245,68 @@ __global__ void __launch_bounds__(Cfg<kPacked>::kThreads, 1)
                 const int uses = set ? used[1]++ : used[0]++;
                 if (!wait(C::kSFree + set, uses + 1)) return false;
                 const uint32_t dS = tmem + kTmemS + kHeads * set;
-#pragma unroll 1
-                for (int c = 0; c < kQChunks; ++c) {
-                    if (t == j0 && !wait(C::kQFull + c, n_pass)) return false;
-                    const bool key = kPacked && c == 8;  // the packed rows' keys
-                    const int st = n % C::kRing;
-                    if (!(key ? wait(C::kKeyFull, n_load) : wait(C::kChFull + st, n / C::kRing))) return false;
-                    tc_fence_after();
-                    if (elect_one()) {
-                        const uint64_t dB = dQ + ((c * kChunkBytes) >> 4);
-                        if (kPacked && !key) {
+                if constexpr (kPacked) {
+                    // The unpacking warps are up to a tile ahead, so this warp's own
+                    // latency is what a tile takes: a wait for every chunk, with its
+                    // 160 cycles, and a rolled loop made 530 cycles a chunk of the 256
+                    // that its products need.  So lane c looks at chunk c's barriers, all
+                    // in one test, and the chunks found in place are issued without more.
+                    // A chunk that was not is waited for.
+                    uint32_t ready = 0;
 #pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                mma_f16_ts(dS, tmem + kTmemRing + 32 * st + 8 * k, dB + ((32 * k) >> 4), idS, (c | k) ? 1u : 0u);
-                        } else {
-                            const uint64_t dA = key ? dRing : dRing + ((st * kChunkBytes) >> 4);
+                    for (int c = 0; c < kQChunks; ++c) {
+                        const bool key = c == 8;
+                        if (!(ready >> c & 1u)) {
+                            bool there = false;
+                            if (lane < kQChunks) {
+                                there = mbar_test(bar(lane == 8 ? (int)C::kKeyFull : (int)C::kChFull + lane), n & 1);
+                                if (t == j0) there = there && mbar_test(bar(C::kQFull + lane), n_pass & 1);
+                            }
+                            ready = __ballot_sync(0xffffffffu, there);
+                            if (!(ready >> c & 1u)) {
+                                if (t == j0 && !wait(C::kQFull + c, n_pass)) return false;
+                                if (!wait(key ? (int)C::kKeyFull : (int)C::kChFull + c, n)) return false;
+                                ready |= 1u << c;
+                            }
+                            __syncwarp();
+                            tc_fence_after();
+                        }
+                        if (elect_one()) {
+                            const uint64_t dB = dQ + ((c * kChunkBytes) >> 4);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                if (key) mma_f16_ss(dS, dRing + ((32 * k) >> 4), dB + ((32 * k) >> 4), idS, 1u);
+                                else mma_f16_ts(dS, tmem + kTmemRing + 32 * c + 8 * k, dB + ((32 * k) >> 4), idS, (c | k) ? 1u : 0u);
+                            }
+                            mma_commit(key ? bar(C::kKeyEmpty) : bar(C::kChEmpty + c));
+                            if (t == j1 - 1) mma_commit(bar(C::kQEmpty + c));
+                            if (key) mma_commit(bar(C::kSFull + set));
+                        }
+                        __syncwarp();
+                    }
+                    ++n;
+                } else {
+#pragma unroll 1
+                    for (int c = 0; c < kQChunks; ++c, ++n) {
+                        if (t == j0 && !wait(C::kQFull + c, n_pass)) return false;
+                        const int st = n % C::kRing;
+                        if (!wait(C::kChFull + st, n / C::kRing)) return false;
+                        tc_fence_after();
+                        if (elect_one()) {
+                            const uint64_t dA = dRing + ((st * kChunkBytes) >> 4), dB = dQ + ((c * kChunkBytes) >> 4);
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
                                 mma_f16_ss(dS, dA + ((32 * k) >> 4), dB + ((32 * k) >> 4), idS, (c | k) ? 1u : 0u);
+                            mma_commit(bar(C::kChEmpty + st));
+                            if (t == j1 - 1) mma_commit(bar(C::kQEmpty + c));
+                            if (c == kQChunks - 1) mma_commit(bar(C::kSFull + set));
                         }
-                        mma_commit(key ? bar(C::kKeyEmpty) : bar(C::kChEmpty + st));
-                        if (t == j1 - 1) mma_commit(bar(C::kQEmpty + c));
-                        if (c == kQChunks - 1) mma_commit(bar(C::kSFull + set));
+                        __syncwarp();
                     }
-                    __syncwarp();
-                    if (key) ++n_load;  // (tiles' keys multiplied)
-                    else ++n;
                 }
             }
             return true;
         });
-        n_load = 0;
     } else if (kPacked && warp >= 12) {
         // ======================================================== unpacking warps: a row a lane, into the row's own TMEM lane
         // Warps 12-15 take the even chunks, 16-19 the odd ones.
@@ -287,36 +318,43 @@ __global__ void __launch_bounds__(Cfg<kPacked>::kThreads, 1)
             for (int t = j0; t < j1; ++t, ++n) {
                 // Every warp waits for both halves of the tile and returns both, though
                 // it reads one: a barrier's parity only tells its phases apart to who
-                // has seen the one before.
-                const int u0 = 2 * n, u1 = 2 * n + 1, st = (u0 + hi) % C::kRawStages;
-                if (!wait(C::kRawFull + u0 % C::kRawStages, u0 / C::kRawStages) ||
-                    !wait(C::kRawFull + u1 % C::kRawStages, u1 / C::kRawStages))
+                // has seen the one before.  It returns them as soon as its codes are in
+                // registers: held until the last chunk was unpacked, they left room for
+                // half a tile ahead.
+                const int st0 = 2 * n % C::kRawStages, st1 = (2 * n + 1) % C::kRawStages;
+                if (!wait(C::kRawFull + st0, 2 * n / C::kRawStages) || !wait(C::kRawFull + st1, (2 * n + 1) / C::kRawStages))
                     return false;
-                if (lane == 0) mbar_arrive(bar(C::kRawEmpty + (u1 - hi) % C::kRawStages));
-                const uint32_t src = base + C::kOffRaw + st * kRawBytes + (32 * (quarter & 1) + lane) * kRawRow;
-                RawChunk r;
-                r.load(src, odd);
-#pragma unroll 1
-                for (int c = odd; c < 8; c += 2) {
+                const uint32_t src = base + C::kOffRaw + (hi ? st1 : st0) * kRawBytes + (32 * (quarter & 1) + lane) * kRawRow;
+                RawChunk r[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) r[k].load(src, odd + 2 * k);
+                __threadfence_block();  // (the loads are neither moved nor done again behind the arrivals)
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(bar(C::kRawEmpty + st0));
+                    mbar_arrive(bar(C::kRawEmpty + st1));
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int c = odd + 2 * k;
                     if (!wait(C::kChEmpty + c, n + 1)) return false;
                     tc_fence_after();
-                    uint32_t v[32];
 #pragma unroll
-                    for (int g = 0; g < 4; ++g) {
-                        uint32_t x[8];
-                        unpack16<false>(r.w[2 * g], r.w[2 * g + 1], (r.scales >> (8 * g)) & 0xFFu, x);
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t v[16];
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) v[8 * g + j] = x[j];
+                        for (int g = 0; g < 2; ++g) {
+                            uint32_t x[8];
+                            unpack16<false>(r[k].w[4 * h + 2 * g], r[k].w[4 * h + 2 * g + 1], (r[k].scales >> (16 * h + 8 * g)) & 0xFFu, x);
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) v[8 * g + j] = x[j];
+                        }
+                        tmem_st16(tmem + lane_addr + kTmemRing + 32 * c + 16 * h, v);
                     }
-                    tmem_st32(tmem + lane_addr + kTmemRing + 32 * c, v);
-                    if (c + 2 < 8) r.load(src, c + 2);
                     tmem_wait_st();
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(bar(C::kChFull + c));
-                        if (c >= 6) mbar_arrive(bar(C::kRawEmpty + st));
-                    }
+                    if (lane == 0) mbar_arrive(bar(C::kChFull + c));
                 }
             }
             return true;
