@@ -598,7 +598,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (rank == 1 && softmax_warp) {
         // ======================================================== accumulator: rescale / epilogue warps
-        const float* slots = reinterpret_cast<const float*>(base_ptr + kOffSlots);
+        // (volatile: read once and here, as the slot is written anew once the warps have arrived)
+        const volatile float* slots = reinterpret_cast<const volatile float*>(base_ptr + kOffSlots);
         const uint32_t o_addr = tmem + lane_addr + 256 * kh;
         int u = 0;
         for (int seg = 0; ok && it.next(seq, T, k0, k1, whole); ++seg) {
@@ -608,9 +609,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (; u < u1; ++u) {
                 const int slot = u % kSlots;
                 if (!wait_peer(kPFull + slot, u / kSlots) || *abort_flag) { ok = false; break; }
-                const float* rowdat = slots + (slot * kSlotBytes + kSlotP) / 4 + 2 * m;
-                const float f = rowdat[0];
-                l_sum = ((u - u0) & 1) ? l_sum + rowdat[1] : rowdat[1];
+                const volatile float* rowdat = slots + (slot * kSlotBytes + kSlotP) / 4 + 2 * m;
+                const float f = rowdat[0], l_part = rowdat[1];
+                l_sum = ((u - u0) & 1) ? l_sum + l_part : l_part;
                 if (u > u0 && __any_sync(0xffffffffu, f != 1.0f)) {
                     // O must hold everything before this unit when it is rescaled
                     if (!wait(kPDone + (u - 1) % kSlots, (u - 1) / kSlots)) { ok = false; break; }
