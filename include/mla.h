@@ -358,7 +358,8 @@ int mla_attend_latent_lse(const mla_dims_t* dims, const void* q_hat, const mla_c
  *   prev    [B][weights_stride] fp32, may be weights itself, or NULL (zero)
  *   weights [B][weights_stride] fp32; entries of rows >= seqlens[b], and of a
  *           sequence with an invalid length (flags MLA_STATUS_BAD_SEQLEN), are left as they were
- * weights_stride >= T_max.  The sums do not depend on how the work is spread (no atomics).
+ * weights_stride >= T_max.  The same call gives the same sums (no atomics); the order in which
+ * several queries' parts are added depends on B, q_len and T_max alone.
  * prev and weights must not overlap otherwise.  Of the options, path,
  * wait_limit_ns and withhold_tile apply. */
 int mla_accumulate_weights(const mla_dims_t* dims, const void* q_hat, const float* lse, const mla_cache_t* cache,

@@ -404,13 +404,69 @@ cudaError_t sm100_attend_packed(const Problem& p, const void* q_hat, const Cache
     return launch_pdl(pk::packed_merge_kernel<8, 2>, dim3(tokens * (kHeads / 8)), dim3(512), 0, st, 1, m);
 }
 
+// How many CTAs of a cluster share the queries of a tile (see sm100_weights.cuh),
+// and the clusters that run at once: the split with the least estimated time, in
+// tiles, of which one takes 2.6 us, a pass over a block `pass` more for Q-hat's
+// load, and the joining of a cluster's sums `join`.  A cluster's range must fit
+// the eight tiles whose sums it holds, by the cache's size, as the lengths lie on
+// the device.  One CTA against a cluster, in us: 1 x 600 packed rows with 16
+// queries 55 and 13, 1 x 4096 with 2 11.2 and 9.3, with 16 56 and 23; but 16 x
+// 2000 with 2 15.6 and 18.0, which the rule leaves to one.
 template <bool kPacked>
-static cudaError_t weights_launch(const CUtensorMap& mQ, const CUtensorMap& mRows, const CUtensorMap& mKey, const wt::Args& a,
-                                  cudaStream_t st) {
+static void weights_split(const Problem& p, int T_max, int* ranks, int* clusters) {
+    using C = wt::Cfg<kPacked>;
+    static int most[4][kMaxDev];  // clusters of 2, 4 and 8 CTAs that run at once (0: not asked yet)
+    const int sms = device_sm_count();
+    *ranks = 1;
+    *clusters = sms;
+    int dev = 0;
+    if (p.q_len == 1 || cudaGetDevice(&dev) != cudaSuccess || dev >= kMaxDev) return;
+    constexpr double pass = 0.2, join = 0.75;
+    const int64_t units = (int64_t)p.B * ((T_max + wt::kTile - 1) / wt::kTile + 1);  // (one more a sequence, as plan_share has it)
+    const int64_t alone = (units + sms - 1) / sms;
+    double best = p.q_len * (double)(alone + pass * ((alone + wt::kBlock - 1) / wt::kBlock));
+    for (int k = 1; k <= 3 && (1 << k) <= p.q_len; ++k) {
+        int& n = most[k][dev];
+        if (n == 0) {
+            cudaLaunchConfig_t cfg;
+            memset(&cfg, 0, sizeof(cfg));
+            cudaLaunchAttribute attr;
+            attr.id = cudaLaunchAttributeClusterDimension;
+            attr.val.clusterDim.x = 1 << k;
+            attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+            cfg.gridDim = dim3((sms >> k) << k);
+            cfg.blockDim = dim3(C::kThreads);
+            cfg.dynamicSmemBytes = C::kSmem;
+            cfg.attrs = &attr;
+            cfg.numAttrs = 1;
+            int found = 0;
+            if (cudaOccupancyMaxActiveClusters(&found, wt::weights_kernel<kPacked>, &cfg) != cudaSuccess || found < 1) {
+                cudaGetLastError();
+                found = -1;
+            }
+            n = found;
+        }
+        if (n < 1) continue;
+        const int64_t share = (units + n - 1) / n;
+        if (share > wt::kBlock) continue;
+        const double t = ((p.q_len + (1 << k) - 1) >> k) * (share + pass) + join;
+        if (t < best) {
+            best = t;
+            *ranks = 1 << k;
+            *clusters = n;
+        }
+    }
+}
+
+template <bool kPacked>
+static cudaError_t weights_launch(const CUtensorMap& mQ, const CUtensorMap& mRows, const CUtensorMap& mKey, const Problem& p,
+                                  wt::Args& a, cudaStream_t st) {
     using C = wt::Cfg<kPacked>;
     cudaError_t e = set_smem(wt::weights_kernel<kPacked>, C::kSmem, g_smem_weights[kPacked]);
     if (e != cudaSuccess) return e;
-    return launch_pdl(wt::weights_kernel<kPacked>, dim3(device_sm_count()), dim3(C::kThreads), C::kSmem, st, 1, mQ, mRows, mKey, a);
+    int clusters;
+    weights_split<kPacked>(p, a.T_max, &a.ranks, &clusters);
+    return launch_pdl(wt::weights_kernel<kPacked>, dim3(clusters * a.ranks), dim3(C::kThreads), C::kSmem, st, a.ranks, mQ, mRows, mKey, a);
 }
 
 cudaError_t sm100_weights(const Problem& p, bool packed, const void* q_hat, const float* lse, const CacheView& cache,
@@ -448,7 +504,7 @@ cudaError_t sm100_weights(const Problem& p, bool packed, const void* q_hat, cons
     a.status = status;
     a.wait_limit_ns = (opts && opts->wait_limit_ns > 0) ? (uint64_t)opts->wait_limit_ns : MLA_WAIT_LIMIT_NS;
     a.withhold_tile = (opts && opts->withhold_tile > 0) ? opts->withhold_tile : -1;
-    return packed ? weights_launch<true>(mQ, mRows, mKey, a, st) : weights_launch<false>(mQ, mRows, mKey, a, st);
+    return packed ? weights_launch<true>(mQ, mRows, mKey, p, a, st) : weights_launch<false>(mQ, mRows, mKey, p, a, st);
 }
 
 cudaError_t sm100_project_small(const Problem& p, void* attend_workspace, int num_pairs, const void* o_lat,

@@ -16,11 +16,15 @@
 // SM against 1.4 us of products); 354 for packed rows: the tensor cores.
 //
 // Split.  The tiles of all sequences are cut into equal ranges, one CTA an SM;
-// a tile is one CTA's for all queries, so a row's sum is always formed in the
-// same order.  With several queries a CTA goes through its range in blocks of
+// a tile is one CTA's for all queries, so a row's sum is formed in one order and
+// needs no atomics.  With several queries a CTA goes through its range in blocks of
 // eight tiles, query by query, so that the rows' second and later readings
 // come from L2; the sums of a block wait in shared memory.  Two sets of four
 // warps take alternate tiles of a block.
+// Where there are fewer tiles than SMs a query after the other would leave most
+// of the SMs idle: there a cluster of CTAs (args.ranks) has a range of at most
+// eight tiles, each CTA takes some of the queries, and at the end the CTAs' sums
+// are added up through distributed shared memory, in the order of their ranks.
 //
 // Measured (B200, bursts): 1 x 4096 full-width rows 11 us (two thirds of it the
 // launch, Q-hat's load and the end); 8 x 65536..131072 rows 187 us, 5.1 TB/s, 0.79
@@ -94,6 +98,7 @@ struct Args {
     int64_t stride_w;
     float decay, scale_log2;
     int B, q_len, T_max;
+    int ranks;          // CTAs of a cluster that share the queries (1: no cluster)
     int* status;
     uint64_t wait_limit_ns;
     int withhold_tile;  // test hook (>= 0): the loader stops before this 64-row tile (see mla.h)
@@ -118,6 +123,7 @@ __global__ void __launch_bounds__(Cfg<kPacked>::kThreads, 1)
     const uint64_t lim = args.wait_limit_ns;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int q_len = args.q_len;
+    const int ranks = args.ranks, group = blockIdx.x / ranks, rank = blockIdx.x % ranks;
 
     if (threadIdx.x == 0) {
         auto init = [&](int first, int n, int count) {
@@ -146,7 +152,7 @@ __global__ void __launch_bounds__(Cfg<kPacked>::kThreads, 1)
     }
     pdl_wait();
     const Batch batch = {args.seqlens, args.B, q_len, args.T_max, kTile, 1};
-    plan_share(batch, gridDim.x, blockIdx.x, 1, false, s_scratch, &s_share);
+    plan_share(batch, gridDim.x / ranks, group, 1, false, s_scratch, &s_share);
     Pieces it(&s_share);
     for (int b = blockIdx.x + gridDim.x * threadIdx.x; b < args.B; b += gridDim.x * blockDim.x)
         if (!batch.valid(batch.len(b))) atomicOr(args.status, MLA_STATUS_BAD_SEQLEN);
@@ -159,14 +165,16 @@ __global__ void __launch_bounds__(Cfg<kPacked>::kThreads, 1)
     bool ok = true, whole = false;
     int seq = 0, T = 0, k0 = 0, k1 = 0;
     int n_load = 0, n_pass = 0;  // loads and passes (query tokens of a block) begun
+    int n_done = 0;              // tiles of the pieces before
     // Every role walks the same passes: tiles j0..j1-1 of a sequence against one of its query tokens.
     auto walk = [&](auto&& pass) {
         while (ok && it.next(seq, T, k0, k1, whole)) {
             const int step = q_len > 1 ? kBlock : k1 - k0;
             for (int j0 = k0; j0 < k1 && ok; j0 += step) {
                 const int j1 = j0 + step < k1 ? j0 + step : k1;
-                for (int i = 0; i < q_len && ok; ++i, ++n_pass) ok = pass(j0, j1, i) && !*abort_flag;
+                for (int i = rank; i < q_len && ok; i += ranks, ++n_pass) ok = pass(j0, j1, i) && !*abort_flag;
             }
+            n_done += k1 - k0;
         }
     };
 
@@ -407,12 +415,12 @@ __global__ void __launch_bounds__(Cfg<kPacked>::kThreads, 1)
                 // query i sees rows 0..T-q_len+i; what a row past it holds reached only its own lane
                 const int r = t * kTile + row;
                 float w = r < T - q_len + 1 + i ? w0 + w1 : 0.f;
-                if (q_len > 1) {
-                    float* s = sums + (t - j0) * kTile + row;
-                    if (i > 0) w += *s;
+                if (q_len > 1) {  // (a cluster's range fits the block: every tile has a place of its own)
+                    float* s = sums + ((ranks > 1 ? n_done : 0) + t - j0) * kTile + row;
+                    if (i > rank) w += *s;
                     *s = w;
                 }
-                if (i == q_len - 1 && r < T) {
+                if (ranks == 1 && i == q_len - 1 && r < T) {
                     const size_t at = (size_t)seq * args.stride_w + r;
                     args.weights[at] = args.prev ? fmaf(args.decay, args.prev[at], w) : w;
                 }
@@ -437,6 +445,27 @@ __global__ void __launch_bounds__(Cfg<kPacked>::kThreads, 1)
     tc_fence_before();
     __syncthreads();
     if (warp == 1) tmem_dealloc(tmem, kTmemCols);
+    if (ranks == 1) return;
+
+    // ---- the cluster's sums: CTA k adds up tiles k, k + ranks, ...
+    cluster_sync();
+    bool any_aborted = false;
+    for (int k = 0; k < ranks; ++k) any_aborted |= ld_shared_cluster_u32(mapa(bar(C::kBars + 1), k)) != 0;
+    Pieces fin(&s_share);
+    int n = 0;
+    while (!any_aborted && fin.next(seq, T, k0, k1, whole)) {
+        for (int t = k0; t < k1; ++t, ++n) {
+            const int r = t * kTile + (int)threadIdx.x;
+            if (n % ranks != rank || threadIdx.x >= kTile || r >= T) continue;
+            const uint32_t place = base + C::kOffSums + (n * kTile + threadIdx.x) * 4;
+            float w = 0.f;
+            for (int k = 0; k < ranks; ++k) w += __uint_as_float(ld_shared_cluster_u32(mapa(place, k)));
+            const size_t at = (size_t)seq * args.stride_w + r;
+            args.weights[at] = args.prev ? fmaf(args.decay, args.prev[at], w) : w;
+        }
+    }
+    __syncthreads();
+    cluster_sync();  // (no CTA's shared memory is read after this)
 }
 
 }  // namespace wt

@@ -131,6 +131,36 @@ def test_weights_expired_wait(lib, packed, T, q_len):
 
 
 @pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("T,q_len", [((5,), 2), ((300,), 3), ((128, 900, 257), 4), ((600,), 5), ((1000, 16, 31), 16), ((2500, 2500), 8),
+                                     ((4096,), 16)])
+def test_weights_queries_shared_by_a_cluster(lib, T, q_len, packed):
+    """Few tiles and several queries: a cluster's CTAs take the queries of a tile between them.  The same sequences in a cache so
+    large that one CTA takes them all give the same sums (added up in another order)."""
+    dims, cache, rows, q, lse, w, before, scale = weights_case(lib, V3, T, q_len, packed, T_max=max(T) + 3)
+    assert lib.device_status() == 0 and lib.last_path() == "sm100"
+    check_weights(w, before, 1.0, q, lse, rows, T, q_len, scale)
+    again = torch.full_like(w, -1.0)
+    lib.accumulate_weights(dims, q, lse, cache, i32(*T), again, prev=None)
+    twice = torch.full_like(w, -1.0)
+    lib.accumulate_weights(dims, q, lse, cache, i32(*T), twice, prev=None)
+    assert torch.equal(again, twice)
+    wide = torch.zeros(len(T), 60000, cache.shape[2], dtype=cache.dtype, device="cuda")
+    wide[:, :cache.shape[1]] = cache
+    one = torch.full((len(T), 60000), -1.0, device="cuda")
+    lib.accumulate_weights(dims, q, lse, wide, i32(*T), one)
+    assert lib.device_status() == 0
+    n = cache.shape[1]
+    # the terms are the same; up to q_len partial sums are added in another order, each step off by 2^-24 of at most the sum
+    assert torch.all((again - one[:, :n]).abs() <= 2 * q_len * 2.0 ** -24 * one[:, :n].abs())
+    assert torch.all(one[:, n:] == -1)
+    # a wait that runs out in some CTA of a cluster ends all of them in order
+    lib.accumulate_weights(dims, q, lse, cache, i32(*T), torch.zeros_like(w), opts=lib.opts(wait_limit_ns=50_000_000, withhold_tile=1))
+    assert lib.device_status() & 4 or max(T) <= 64
+    lib.accumulate_weights(dims, q, lse, cache, i32(*T), twice)
+    assert lib.device_status() == 0 and torch.equal(again, twice)
+
+
+@pytest.mark.parametrize("packed", [False, True])
 def test_weights_of_many_short_sequences(lib, packed):
     # more sequences than a block has threads, some invalid: every valid sequence's weights add up to its queries and heads
     B, T_max, q_len = 1500, 200, 2
