@@ -18,7 +18,7 @@
 // Split.  The tiles of all sequences are cut into equal ranges, one CTA an SM;
 // a tile is one CTA's for all queries, so a row's sum is formed in one order and
 // needs no atomics.  With several queries a CTA goes through its range in blocks of
-// eight tiles, query by query, so that the rows' second and later readings
+// up to eight tiles, query by query, so that the rows' second and later readings
 // come from L2; the sums of a block wait in shared memory.  Two sets of four
 // warps take alternate tiles of a block.
 // Where there are fewer tiles than SMs a query after the other would leave most
@@ -51,7 +51,7 @@ constexpr int kTile = 128;                // rows of a tile
 constexpr int kUnit = 64;                 // rows of a raw copy
 constexpr int kChunkBytes = kTile * 128;  // 128 rows x 64 bf16, SW128
 constexpr int kQChunks = 9;
-constexpr int kBlock = 8;                 // tiles of a block when there are several queries
+constexpr int kBlock = 8;                 // most tiles of a block when there are several queries
 constexpr int kRawRow = kPackNib + kPackScale;
 constexpr int kRawBytes = kUnit * kRawRow;  // 18 KB: 64 raw rows
 constexpr int kSetWarps = 4;
@@ -61,6 +61,11 @@ struct Cfg {
     static constexpr int kThreads = kPacked ? 640 : 384;
     static constexpr int kRing = kPacked ? 8 : 4;  // chunks: TMEM columns / shared memory
     static constexpr int kRawStages = 3;
+    // Blocks where a CTA has more than one: those of all CTAs have to stay in L2
+    // until the last query has read them.  Eight tiles of full-width rows on every
+    // SM are 175 MB: 9 x 56330 rows with two queries 199 us, in blocks of two 177
+    // (four 184, one 215); of packed rows, 63 MB, no difference.
+    static constexpr int kLongBlock = kPacked ? kBlock : 2;
     static constexpr int kOffRing = kQChunks * kChunkBytes;
     // packed: the keys' chunk, then the raw stages; full width: the ring
     static constexpr int kOffRaw = kOffRing + kChunkBytes;
@@ -169,7 +174,7 @@ __global__ void __launch_bounds__(Cfg<kPacked>::kThreads, 1)
     // Every role walks the same passes: tiles j0..j1-1 of a sequence against one of its query tokens.
     auto walk = [&](auto&& pass) {
         while (ok && it.next(seq, T, k0, k1, whole)) {
-            const int step = q_len > 1 ? kBlock : k1 - k0;
+            const int step = q_len == 1 ? k1 - k0 : (s_share.L > kBlock ? C::kLongBlock : kBlock);
             for (int j0 = k0; j0 < k1 && ok; j0 += step) {
                 const int j1 = j0 + step < k1 ? j0 + step : k1;
                 for (int i = rank; i < q_len && ok; i += ranks, ++n_pass) ok = pass(j0, j1, i) && !*abort_flag;

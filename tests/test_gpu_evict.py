@@ -160,6 +160,24 @@ def test_weights_queries_shared_by_a_cluster(lib, T, q_len, packed):
     assert lib.device_status() == 0 and torch.equal(again, twice)
 
 
+@pytest.mark.parametrize("q_len", [2, 3])
+def test_weights_of_ranges_of_several_blocks(lib, q_len):
+    # more than eight tiles a CTA: blocks of two, which end inside sequences and ranges; against the CUDA-core path
+    T = torch.randint(3000, 4701, (48,), generator=torch.Generator().manual_seed(6))
+    dims, seq, T_max = dims_of(lib, V3), T.to(torch.int32).cuda(), 4700
+    cache = rand(3, 48, T_max, 576, dtype=torch.bfloat16)
+    q = rand(2, 48, q_len, 128, 576, dtype=torch.bfloat16, std=0.05)
+    lse = torch.zeros(48, q_len, 128, device="cuda")
+    lib.attend_latent_lse(dims, q, cache, seq, lse)
+    w, v = torch.full((48, T_max), -1.0, device="cuda"), torch.full((48, T_max), -1.0, device="cuda")
+    lib.accumulate_weights(dims, q, lse, cache, seq, w)
+    assert lib.last_path() == "sm100"
+    lib.accumulate_weights(dims, q, lse, cache, seq, v, opts=lib.opts(path=2))
+    assert lib.device_status() == 0
+    past = torch.arange(T_max, device="cuda") >= seq[:, None]
+    assert torch.all(w[past] == -1) and torch.all((w - v).abs() <= 2e-4 * v.abs() + 1e-6)
+
+
 @pytest.mark.parametrize("packed", [False, True])
 def test_weights_of_many_short_sequences(lib, packed):
     # more sequences than a block has threads, some invalid: every valid sequence's weights add up to its queries and heads
