@@ -612,7 +612,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const volatile float* rowdat = slots + (slot * kSlotBytes + kSlotP) / 4 + 2 * m;
                 const float f = rowdat[0], l_part = rowdat[1];
                 l_sum = ((u - u0) & 1) ? l_sum + l_part : l_part;
-                if (u > u0 && __any_sync(0xffffffffu, f != 1.0f)) {
+                // (the vote has both values, so that neither load is under way when the slot is given back; a sum is never negative)
+                const bool scaled = __any_sync(0xffffffffu, f != 1.0f || l_part < 0.f);
+                if (u > u0 && scaled) {
                     // O must hold everything before this unit when it is rescaled
                     if (!wait(kPDone + (u - 1) % kSlots, (u - 1) / kSlots)) { ok = false; break; }
                     tc_fence_after();

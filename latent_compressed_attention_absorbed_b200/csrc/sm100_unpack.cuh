@@ -89,6 +89,16 @@ struct RawChunk {
         ld_shared_v4u(raw_row + 32 * c, w[0], w[1], w[2], w[3]);
         ld_shared_v4u(raw_row + 32 * c + 16, w[4], w[5], w[6], w[7]);
     }
+    // The same by loads that the compiler keeps where they stand and does once.
+    __device__ __forceinline__ void load_once(uint32_t raw_row, int c) {
+        asm volatile("ld.volatile.shared.b32 %0, [%1];" : "=r"(scales) : "r"(raw_row + kPackNib + 4 * c) : "memory");
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            asm volatile("ld.volatile.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(w[4 * h]), "=r"(w[4 * h + 1]), "=r"(w[4 * h + 2]), "=r"(w[4 * h + 3])
+                         : "r"(raw_row + 32 * c + 16 * h)
+                         : "memory");
+    }
     // -> 128 bytes of values at row `row` of a swizzled chunk of 128-byte rows.
     // at: the row's first piece, chunk + 128 row + 16 (row % 8); piece j lies at
     // at ^ 16 j (the chunk starts on a 1024-byte boundary).

@@ -325,6 +325,7 @@ __global__ void __launch_bounds__(Cfg<kPacked>::kThreads, 1)
         // Warps 12-15 take the even chunks, 16-19 the odd ones.
         const int quarter = warp & 3, odd = warp >= 16 ? 1 : 0, hi = quarter >> 1;
         const uint32_t lane_addr = (uint32_t)(quarter * 32) << 16;
+        const uint32_t never = (uint32_t)(q_len >> 31);  // 0, which the compiler does not know
         int n = 0;  // tiles
         walk([&](int j0, int j1, int) {
 #pragma unroll 1
@@ -340,10 +341,13 @@ __global__ void __launch_bounds__(Cfg<kPacked>::kThreads, 1)
                 const uint32_t src = base + C::kOffRaw + (hi ? st1 : st0) * kRawBytes + (32 * (quarter & 1) + lane) * kRawRow;
                 RawChunk r[4];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) r[k].load(src, odd + 2 * k);
-                __threadfence_block();  // (the loads are neither moved nor done again behind the arrivals)
-                __syncwarp();
-                if (lane == 0) {
+                for (int k = 0; k < 4; ++k) r[k].load_once(src, odd + 2 * k);
+                // An arrival overtakes loads that are still queued, and the next rows would
+                // land under them: the vote has a word of every load, so it waits for all.
+                uint32_t some = 0;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) some |= r[k].scales | r[k].w[0] | r[k].w[4];
+                if (!__any_sync(0xffffffffu, (some & never) != 0) && lane == 0) {
                     mbar_arrive(bar(C::kRawEmpty + st0));
                     mbar_arrive(bar(C::kRawEmpty + st1));
                 }

@@ -160,6 +160,43 @@ def test_weights_queries_shared_by_a_cluster(lib, T, q_len, packed):
     assert lib.device_status() == 0 and torch.equal(again, twice)
 
 
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("B,T_max,q_len", [(300, 700, 3), (1500, 200, 2)])
+def test_weights_again_and_again(lib, packed, B, T_max, q_len):
+    # a row that is overwritten while it is still being read shows once in hundreds of calls
+    dims = dims_of(lib, V3)
+    T = torch.randint(q_len, T_max + 1, (B,), generator=torch.Generator().manual_seed(5)).to(torch.int32).cuda()
+    q = rand(2, B, q_len, 128, 576, dtype=torch.bfloat16, std=0.25)
+    lse = torch.full((B, q_len, 128), 5.0, device="cuda")
+    if packed:
+        cache = torch.randint(0, 256, (B, T_max, 416), generator=torch.Generator(device="cuda").manual_seed(1), device="cuda", dtype=torch.uint8)
+        cache[:, :, 256:288] = 160
+        cache[:, :, 288:] = rand(4, B, T_max, 64, dtype=torch.bfloat16).view(torch.uint8)
+    else:
+        cache = rand(3, B, T_max, 576, dtype=torch.bfloat16)
+    first = lib.accumulate_weights(dims, q, lse, cache, T, torch.zeros(B, T_max, device="cuda"))
+    w, differ = torch.empty_like(first), torch.zeros((), dtype=torch.int64, device="cuda")
+    for _ in range(1000):
+        w.zero_()
+        lib.accumulate_weights(dims, q, lse, cache, T, w)
+        differ += (w != first).any()
+    assert torch.isfinite(first).all() and differ.item() == 0 and lib.device_status() == 0
+
+
+@pytest.mark.parametrize("T,q_len", [((4096,), 1), ((700, 333, 5, 1200), 2)])
+def test_packed_attention_again_and_again(lib, T, q_len):
+    dims = dims_of(lib, V3)
+    cache, _ = make_cache(lib, dims, V3, T)
+    q = rand(2, len(T), q_len, 128, 576, dtype=torch.bfloat16, std=0.25)
+    first = lib.attend_packed(dims, q, cache, i32(*T))
+    out, seq, differ = torch.empty_like(first), i32(*T), torch.zeros((), dtype=torch.int64, device="cuda")
+    for _ in range(1000):
+        out.zero_()
+        lib.attend_packed(dims, q, cache, seq, out=out)
+        differ += (out != first).any()
+    assert differ.item() == 0 and lib.device_status() == 0
+
+
 @pytest.mark.parametrize("q_len", [2, 3])
 def test_weights_of_ranges_of_several_blocks(lib, q_len):
     # more than eight tiles a CTA: blocks of two, which end inside sequences and ranges; against the CUDA-core path
