@@ -29,8 +29,8 @@
 // Measured (B200, bursts): 1 x 4096 full-width rows 11 us (two thirds of it the
 // launch, Q-hat's load and the end); 8 x 65536..131072 rows 187 us, 5.1 TB/s, 0.79
 // of the copy's bandwidth (the power limit is reached there, with the clock at
-// 1.24 GHz); 64 x 2048..16384 packed rows with two queries 157 us, 0.67 of the
-// products' rate.
+// 1.24 GHz); 64 x 2048..16384 packed rows with two queries 153 us, 0.69 of the
+// products' rate (181 us in a loop, at the power limit).
 //
 // Every wait is bounded; no warp waits on a barrier without a limit before
 // the common end, so a wait that expires ends the kernel in order.
