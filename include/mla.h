@@ -319,7 +319,9 @@ size_t mla_packed_workspace_bytes(const mla_dims_t* dims, int32_t B, int32_t q_l
 
 /* mla_attend_latent over a packed cache.  lse [B][q_len][H] fp32 (may be
  * NULL) receives the natural log of the sum over keys of exp(s_j), -infinity
- * for a sequence with an invalid length.  Of the options, path, num_pairs,
+ * for a sequence with an invalid length and where every score is -infinity
+ * (o_lat is zero there).  A NaN among a query's scores, or +infinity, makes
+ * its o_lat and its lse NaN.  Of the options, path, num_pairs,
  * overhead_tiles and min_tiles (both in 128-key tiles here, 1 by default),
  * wait_limit_ns and withhold_tile apply. */
 int mla_attend_packed(const mla_dims_t* dims, const void* q_hat, const mla_cache_t* cache, const int32_t* seqlens,

@@ -343,8 +343,11 @@ __device__ __forceinline__ uint32_t sw128(int r, int c) { return (uint32_t)(r * 
 __device__ __forceinline__ uint32_t sw64(int r, int c) { return (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3)) << 4)); }
 
 // Natural-log LSE of a row with base-2 maximum m2 and sum l of 2^(s - m2).
+// -infinity says that no key counts; a NaN sum (a NaN score, which the maximum
+// does not show) is a NaN LSE, here and wherever an LSE is formed, hence
+// !(l <= 0) for l > 0.
 __device__ __forceinline__ float lse_natural(float m2, float l) {
-    return l > 0.f ? (m2 + log2f(l)) * 0.6931471805599453f : -CUDART_INF_F;
+    return !(l <= 0.f) ? (m2 + log2f(l)) * 0.6931471805599453f : -CUDART_INF_F;
 }
 
 // Rows at or beyond the sequence length hold no cached token: zero `nchunks`
@@ -736,10 +739,13 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                     float* const dst = w.whole ? args.lse : args.part_lse;
                     if (ok && kh == 0) {
                         const size_t row = (size_t)(w.whole ? w.seq : grp + w.seq) * q_len + qi;
-                        const float v = l_sum > 0.f ? m_used + __log2f(l_sum) : -CUDART_INF_F;
+                        const float v = !(l_sum <= 0.f) ? m_used + __log2f(l_sum) : -CUDART_INF_F;
                         dst[row * kHeads + m] = w.whole ? v * 0.6931471805599453f : v;
                     }
                 } else if (ok && !w.whole && kh == 0) {
+                    // (of a NaN sum this makes -infinity; the partial's columns are NaN then and
+                    // stay so in the merge.  The test written for NaN moved this form's code: 8 x
+                    // 131072 rows 405 -> 409 us)
                     const size_t pslot = (size_t)(grp + w.seq) * q_len + qi;
                     args.part_lse[pslot * kHeads + m] = l_sum > 0.f ? m_used + __log2f(l_sum) : -CUDART_INF_F;
                 }
@@ -1101,11 +1107,11 @@ struct MergeState {
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    // Folds in another state (m2, w2, a2).
+    // Folds in another state (m2, w2, a2).  A NaN in it, or in the state so far,
+    // stays in wsum and acc, although fmaxf drops it.
     __device__ void fold(float m2, float w2, const float4 (&a2)[4]) {
-        const float mb = fmaxf(m, m2);
-        if (mb == -CUDART_INF_F) return;
-        const float r0 = exp2f(m - mb), r1 = exp2f(m2 - mb);  // -inf gives 0
+        const float mb = fmaxf(m, m2), ref = mb == -CUDART_INF_F ? 0.f : mb;
+        const float r0 = exp2f(m - ref), r1 = exp2f(m2 - ref);  // -inf gives 0
         wsum = wsum * r0 + w2 * r1;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -1115,7 +1121,7 @@ struct MergeState {
         m = mb;
     }
     __device__ void normalise() {
-        const float inv = wsum > 0.f ? 1.f / wsum : 0.f;
+        const float inv = !(wsum <= 0.f) ? 1.f / wsum : 0.f;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             acc[j].x *= inv; acc[j].y *= inv; acc[j].z *= inv; acc[j].w *= inv;

@@ -499,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (ok && kh == 0) {
                 if (!whole) {
                     const size_t pslot = (size_t)(grp + seq) * q_len + qi;
-                    args.part_lse[pslot * kHeads + m] = l_sum > 0.f ? m_used - kPShift + log2f(l_sum) : -CUDART_INF_F;
+                    args.part_lse[pslot * kHeads + m] = !(l_sum <= 0.f) ? m_used - kPShift + log2f(l_sum) : -CUDART_INF_F;
                 } else if (args.lse) {
                     args.lse[((size_t)seq * q_len + qi) * kHeads + m] = lse_natural(m_used - kPShift, l_sum);
                 }

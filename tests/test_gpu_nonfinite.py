@@ -1,0 +1,92 @@
+"""NaN and infinities in what an attention sees: a NaN score makes its query's output and log-sum-exp NaN, however the sequence was
+cut and whichever piece holds it, and nothing else changes by a bit.  (A score's NaN does not show in the running maximum, and a cut
+sequence is merged from pieces by their log-sum-exps, so it could be taken for a piece that holds nothing.)"""
+import numpy as np
+import pytest
+import torch
+
+from mla_testutil import as_f64
+from oracle import cache_oracle as co
+from test_gpu_packed import TINY, V3, check_attention, decode_inputs, dims_of, i32, make_cache, rand, stored_rows
+
+pytestmark = pytest.mark.gpu
+
+NAN, INF = float("nan"), float("inf")
+
+
+def poison(cache, g, row, value, element=0):
+    """One element of row `row`'s RoPE key of sequence 0, in a copy of the cache."""
+    H, d_c, d_r, _, _, dt = g
+    out = cache.clone()
+    if cache.dtype == torch.uint8:
+        at = (d_c // 2 + d_c // 16 + 15) // 16 * 16
+        out[0, row, at:at + d_r * dt.itemsize].view(dt)[element] = value
+    else:
+        out[0, row, d_c + element] = value
+    return out
+
+
+def case(lib, g, T, q_len, packed):
+    H, d_c, d_r, _, _, dt = g
+    dims = dims_of(lib, g)
+    cache = make_cache(lib, dims, g, T)[0] if packed else rand(9, len(T), max(T), d_c + d_r, dtype=dt)
+    q = rand(3, len(T), q_len, H, d_c + d_r, dtype=dt, std=0.25)
+    call = lib.attend_packed if packed else lib.attend_latent_lse
+
+    def attend(q, cache, **opts):
+        lse = torch.zeros(len(T), q_len, H, device="cuda")
+        return call(dims, q, cache, i32(*T), lse=lse, opts=lib.opts(**opts)), lse
+    return cache, q, attend
+
+
+def same(a, b):
+    return all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+# whole sequences, cut ones (pieces merged by one warp each and by two), several queries
+CUTS = [((2000,), 1, 1), ((2000,), 1, 16), ((4096, 700), 1, 0), ((900, 77), 2, 16), ((640,) * 7, 1, 8)]
+
+
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("T,q_len,pairs", CUTS)
+def test_nan_in_a_query_head(lib, T, q_len, pairs, packed):
+    cache, q, attend = case(lib, V3, T, q_len, packed)
+    clean = attend(q, cache, num_pairs=pairs)
+    for value in (NAN, INF):
+        bad = q.clone()
+        bad[0, -1, 7, 3] = value            # (an infinity times latents of both signs: scores of both infinities)
+        o, lse = attend(bad, cache, num_pairs=pairs)
+        assert lib.device_status() == 0 and lib.last_path() == "sm100"
+        assert o[0, -1, 7].isnan().all() and lse[0, -1, 7].isnan()
+        o[0, -1, 7], lse[0, -1, 7] = clean[0][0, -1, 7], clean[1][0, -1, 7]
+        assert same((o, lse), clean)
+
+
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("T,q_len,pairs", CUTS)
+def test_nan_in_a_key(lib, T, q_len, pairs, packed):
+    cache, q, attend = case(lib, V3, T, q_len, packed)
+    clean = attend(q, cache, num_pairs=pairs)
+    for row in (0, 300, T[0] // 2, T[0] - q_len):   # in the first, the middle and the last piece, seen by every query
+        o, lse = attend(q, poison(cache, V3, row, NAN), num_pairs=pairs)
+        assert lib.device_status() == 0
+        assert o[0].isnan().all() and lse[0].isnan().all(), f"row {row}"
+        assert same((o[1:], lse[1:]), (clean[0][1:], clean[1][1:]))
+
+
+@pytest.mark.parametrize("T", [(2000,), (2000, 300), (700,) * 12])   # merged by the projection of few rows, by the combine
+def test_nan_in_a_key_through_the_decode(lib, T):
+    dims = dims_of(lib, V3)
+    cache = rand(9, len(T), max(T), 576, dtype=torch.bfloat16)
+    ins = decode_inputs(V3, len(T), 1)
+    clean = lib.decode(dims, *ins, cache, i32(*T))
+    assert clean.isfinite().all()
+    for row in (0, 300, T[0] - 1):
+        out = lib.decode(dims, *ins, poison(cache, V3, row, NAN), i32(*T))
+        assert out[0].isnan().all() and torch.equal(out[1:], clean[1:])
+    packed = make_cache(lib, dims, V3, T)[0]
+    clean = lib.decode_packed(dims, *ins, packed, i32(*T))
+    for row in (0, 300, T[0] - 1):
+        out = lib.decode_packed(dims, *ins, poison(packed, V3, row, NAN), i32(*T))
+        assert out[0].isnan().all() and torch.equal(out[1:], clean[1:])
+    assert lib.device_status() == 0
