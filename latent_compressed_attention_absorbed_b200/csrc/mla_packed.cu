@@ -314,9 +314,10 @@ __global__ void __launch_bounds__(kAttWarps * 32)
 #pragma unroll
         for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
         s *= p.scale;
-        const float m_new = fmaxf(m_run, s);
-        const float corr = expf(m_run - m_new);
-        const float pj = expf(s - m_new);
+        // (a score of -infinity has no weight; a NaN one, which fmaxf drops, makes the sums NaN)
+        const float m_new = fmaxf(m_run, s), ref = m_new == -INFINITY ? 0.f : m_new;
+        const float corr = expf(m_run - ref);
+        const float pj = expf(s - ref);
         l_run = l_run * corr + pj;
 #pragma unroll
         for (int r = 0; r < kMaxPerLane; ++r) {
@@ -338,12 +339,12 @@ __global__ void __launch_bounds__(kAttWarps * 32)
     float M = -INFINITY;
     for (int w = 0; w < kAttWarps; ++w) M = fmaxf(M, sm[w]);
     float L = 0.f;
-    for (int w = 0; w < kAttWarps; ++w) L += (sm[w] == -INFINITY) ? 0.f : sl[w] * expf(sm[w] - M);
+    const float ref = M == -INFINITY ? 0.f : M;
+    for (int w = 0; w < kAttWarps; ++w) L += sl[w] * expf(sm[w] - ref);
     for (int c = threadIdx.x; c < p.d_c; c += blockDim.x) {
         float o = 0.f;
-        for (int w = 0; w < kAttWarps; ++w)
-            if (sm[w] != -INFINITY) o += so[w * p.d_c + c] * expf(sm[w] - M);
-        st(out, c, o / L);
+        for (int w = 0; w < kAttWarps; ++w) o += so[w * p.d_c + c] * expf(sm[w] - ref);
+        st(out, c, L == 0.f ? 0.f : o / L);  // (0: every score is -infinity)
     }
     if (lse && threadIdx.x == 0) lse[(size_t)u * p.H + h] = M + logf(L);
 }

@@ -90,3 +90,70 @@ def test_nan_in_a_key_through_the_decode(lib, T):
         out = lib.decode_packed(dims, *ins, poison(packed, V3, row, NAN), i32(*T))
         assert out[0].isnan().all() and torch.equal(out[1:], clean[1:])
     assert lib.device_status() == 0
+
+
+# ------------------------------------------------------------------ the CUDA-core form, and scores of -infinity in both
+
+GENERIC = [(TINY, (40, 9), 2), (TINY, (3,), 1), (V3, (300, 7), 2)]
+
+
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("g,T,q_len", GENERIC)
+def test_nan_on_cuda_cores(lib, g, T, q_len, packed):
+    cache, q, attend = case(lib, g, T, q_len, packed)
+    clean = attend(q, cache, path=2)
+    for row in (0, 1, T[0] - q_len):                 # (a warp takes every eighth row: alone in it, first, last)
+        o, lse = attend(q, poison(cache, g, row, NAN), path=2)
+        assert lib.last_path() == "generic" and lib.device_status() == 0
+        assert o[0].isnan().all() and lse[0].isnan().all(), f"row {row}"
+        assert same((o[1:], lse[1:]), (clean[0][1:], clean[1][1:]))
+        if not packed:                               # the attention without log-sum-exps has a kernel of its own
+            dims, opts = dims_of(lib, g), lib.opts(path=2)
+            o = lib.attend_latent(dims, q, poison(cache, g, row, NAN), i32(*T), opts=opts)
+            assert o[0].isnan().all() and torch.equal(o[1:], lib.attend_latent(dims, q, cache, i32(*T), opts=opts)[1:])
+            o = lib.attend_latent(dims, q, poison(cache, g, row, -INF), i32(*T), opts=opts)
+            assert torch.equal(o[1:], lib.attend_latent(dims, q, cache, i32(*T), opts=opts)[1:])
+    bad = q.clone()
+    bad[0, -1, 2, 1] = NAN
+    o, lse = attend(bad, cache, path=2)
+    assert o[0, -1, 2].isnan().all() and lse[0, -1, 2].isnan()
+    o[0, -1, 2], lse[0, -1, 2] = clean[0][0, -1, 2], clean[1][0, -1, 2]
+    assert same((o, lse), clean)
+
+
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("g,T,path", [(V3, (900, 70), 0), (V3, (300, 70), 2), (TINY, (40, 9), 2)])
+def test_scores_of_minus_infinity(lib, g, T, path, packed):
+    # such rows have no weight, whether they come first, alone or last; only such rows: zeros and a log-sum-exp of -infinity
+    H, d_c, d_r, d_n, _, dt = g
+    cache, q, attend = case(lib, g, T, 1, packed)
+    q[..., d_c] = q[..., d_c].abs() + 0.01
+    dead = [0, 1, 8, 16, T[0] - 1]
+    low = cache
+    for row in dead:
+        low = poison(low, g, row, -INF)
+    o, lse = attend(q, low, path=path)
+    dims = dims_of(lib, g)
+    rows = stored_rows(lib, dims, cache, T) if packed else [as_f64(cache[b, :t]) for b, t in enumerate(T)]
+    rows[0] = np.delete(rows[0], dead, 0)
+    left = tuple(len(r) for r in rows)
+    if packed or dt == torch.float32:
+        check_attention(o, lse, q, rows, left, 1, g, (d_n + d_r) ** -0.5)
+    else:                                            # (the full-width form holds the weights in bf16)
+        want = [co.attend(as_f64(q)[b, 0], rows[b], t, d_c, (d_n + d_r) ** -0.5) for b, t in enumerate(left)]
+        for b, (wo, wl) in enumerate(want):
+            assert np.linalg.norm(as_f64(o)[b, 0] - wo) <= 5e-3 * np.linalg.norm(wo)
+            assert np.all(np.abs(as_f64(lse)[b, 0] - wl) <= 1e-4 * (1 + np.abs(wl)))
+    all_low = cache
+    for row in range(9):
+        all_low = poison(all_low, g, row, -INF)
+    few = i32(*([9] + list(T[1:])))
+    call = lib.attend_packed if packed else lib.attend_latent_lse
+    z = torch.zeros_like(lse)
+    o = call(dims, q, all_low, few, lse=z, opts=lib.opts(path=path))
+    if not packed:
+        for c, n in ((low, i32(*T)), (all_low, few)):
+            plain = lib.attend_latent(dims, q, c, n, opts=lib.opts(path=path))
+            assert plain.isfinite().all() and (n is not few or not plain[0].any())
+    assert not o[0].any() and torch.all(z[0] == -INF) and o[1:].isfinite().all() and z[1:].isfinite().all()
+    assert lib.device_status() == 0
