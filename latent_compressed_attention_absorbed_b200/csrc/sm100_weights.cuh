@@ -387,10 +387,13 @@ __global__ void __launch_bounds__(Cfg<kPacked>::kThreads, 1)
         int n = 0;  // tiles of this set
         walk([&](int j0, int j1, int i) {
             __syncwarp();
+            bool uncounted = false;
             for (int h = lane; h < kHeads; h += 32) {
                 const float z = args.lse[((size_t)seq * q_len + i) * kHeads + h];
                 nlse[h] = z == -CUDART_INF_F ? -CUDART_INF_F : z * -1.4426950408889634f;
+                uncounted |= z == -CUDART_INF_F;
             }
+            uncounted = __any_sync(0xffffffffu, uncounted);
             __syncwarp();
 #pragma unroll 1
             for (int t = j0 + set; t < j1; t += 2, ++n) {
@@ -402,6 +405,11 @@ __global__ void __launch_bounds__(Cfg<kPacked>::kThreads, 1)
                     uint32_t v[16];
                     tmem_ld16(s_addr + h, v);
                     tmem_wait_ld();
+                    if (uncounted) {  // whatever such a query's score is, infinite or NaN
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            if (ld_shared_u32(nl_addr + 4 * (h + j)) == 0xFF800000u) v[j] = 0u;
+                    }
 #pragma unroll
                     for (int j = 0; j < 16; j += 4) {
                         uint32_t z[4];

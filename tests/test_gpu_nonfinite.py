@@ -157,3 +157,29 @@ def test_scores_of_minus_infinity(lib, g, T, path, packed):
             assert plain.isfinite().all() and (n is not few or not plain[0].any())
     assert not o[0].any() and torch.all(z[0] == -INF) and o[1:].isfinite().all() and z[1:].isfinite().all()
     assert lib.device_status() == 0
+
+
+# ------------------------------------------------------------------ accumulated weights
+
+@pytest.mark.parametrize("path", [0, 2])
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("T,q_len", [((300, 40), 1), ((600,), 5), ((2500, 2500), 2)])
+def test_weights_of_queries_that_count_nothing(lib, T, q_len, packed, path):
+    # a log-sum-exp of -infinity: the query's scores do not matter, not even NaN or infinite ones
+    dims = dims_of(lib, V3)
+    cache, q, _ = case(lib, V3, T, q_len, packed)
+    lse = rand(8, len(T), q_len, 128) + 5
+    lse[0, 0, ::3] = -INF
+    lse[-1, -1, 64:] = -INF
+    want = lib.accumulate_weights(dims, q, lse, cache, i32(*T), torch.zeros(len(T), max(T), device="cuda"), opts=lib.opts(path=path))
+    bad = torch.where((lse == -INF)[..., None], torch.tensor(NAN, device="cuda", dtype=q.dtype), q)
+    bad[0, 0, 3, 9], bad[0, 0, 6] = INF, -INF        # (heads 3 and 6 count nothing)
+    got = lib.accumulate_weights(dims, bad, lse, cache, i32(*T), torch.zeros(len(T), max(T), device="cuda"), opts=lib.opts(path=path))
+    assert lib.device_status() == 0
+    assert want.isfinite().all() and torch.equal(got, want)
+    # a NaN among the scores of a query that counts stays in the sums of the rows it sees
+    bad = q.clone()
+    bad[0, 0, 1, 9] = NAN
+    got = lib.accumulate_weights(dims, bad, lse, cache, i32(*T), torch.zeros(len(T), max(T), device="cuda"), opts=lib.opts(path=path))
+    n = T[0] - q_len + 1
+    assert got[0, :n].isnan().all() and torch.equal(got[0, n:], want[0, n:]) and torch.equal(got[1:], want[1:])
