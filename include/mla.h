@@ -110,7 +110,9 @@ size_t mla_workspace_bytes(const mla_dims_t* dims, int32_t B, int32_t q_len);
  * (q_len = 1 plain decode; 2..16 speculative verify, causal among the new
  * tokens).  seqlens[b] counts cached tokens INCLUDING the q_len new ones,
  * which must already be appended; query i sits at position
- * m = seqlens[b] - q_len + i and attends to keys 0..m.
+ * m = seqlens[b] - q_len + i and attends to keys 0..m.  (The rows of later
+ * new tokens get the weight 0; NaN or infinite latents there still reach the
+ * earlier queries on the sm_100a path.)
  *   q_nope [B][q_len][H][d_n]   content query
  *   q_rope [B][q_len][H][d_r]   UN-rotated RoPE query (rotated here at m)
  *   W_UK   [H][d_n][d_c]        k_C = W_UK[h] c      (U in R^{d_h x d_c})
@@ -349,7 +351,8 @@ int mla_decode_packed(const mla_dims_t* dims, const void* q_nope, const void* q_
  * attend with the row counts. */
 enum { MLA_CACHE_FULL = 0, MLA_CACHE_PACKED = 1 }; /* cache_format */
 
-/* mla_attend_latent that also writes the log-sum-exps, as mla_attend_packed does (lse not NULL). */
+/* mla_attend_latent that also writes the log-sum-exps, as mla_attend_packed does (lse not NULL).  What the rows of later
+ * new tokens hold does not reach a query here. */
 int mla_attend_latent_lse(const mla_dims_t* dims, const void* q_hat, const mla_cache_t* cache, const int32_t* seqlens,
                           int32_t B, int32_t q_len, void* o_lat, float* lse, void* workspace, size_t workspace_bytes,
                           const mla_decode_opts_t* opts, mla_stream_t stream);

@@ -159,6 +159,24 @@ def test_scores_of_minus_infinity(lib, g, T, path, packed):
     assert lib.device_status() == 0
 
 
+# ------------------------------------------------------------------ new tokens past a query
+
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("T,q_len", [((700, 77), 2), ((64, 65, 63, 130), 3), ((16, 300), 16)])
+def test_nan_in_a_token_past_the_query(lib, T, q_len, packed):
+    # only the last query sees the last token: the others' outputs keep their bits
+    cache, q, attend = case(lib, V3, T, q_len, packed)
+    for path in (0, 2):
+        clean = attend(q, cache, path=path)
+        for value in (NAN, INF):
+            bad = poison(cache, V3, T[0] - 1, value)
+            if not packed:
+                bad[0, T[0] - 1, 100:300] = value       # its latents too, as long as they can be NaN
+            o, lse = attend(q, bad, path=path)
+            assert o[0, -1].isnan().any() and lib.device_status() == 0
+            assert same((o[0, :-1], lse[0, :-1], o[1:], lse[1:]), (clean[0][0, :-1], clean[1][0, :-1], clean[0][1:], clean[1][1:]))
+
+
 # ------------------------------------------------------------------ accumulated weights
 
 @pytest.mark.parametrize("path", [0, 2])
