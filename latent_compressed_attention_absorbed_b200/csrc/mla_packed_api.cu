@@ -100,14 +100,29 @@ PackedDecodeLayout packed_decode_layout(const Problem& p) {
     return L;
 }
 
-// First and one-past-last byte a cache view can touch.
+// The bytes a view can touch: B sequences of `rows` rows of `row` bytes.
 struct Span {
-    uintptr_t lo, hi;
-    bool overlaps(const Span& o) const { return lo < o.hi && o.lo < hi; }
+    uintptr_t at;
+    int64_t B, stride_b, rows, stride_t, row;
+    int64_t each() const { return (rows - 1) * stride_t + row; }  // bytes from a sequence's start to its end
+    uintptr_t end() const { return at + (uintptr_t)((B - 1) * stride_b + each()); }
+    // Whether two views may share a byte.  Views of one array that lie between each
+    // other do not: in a common period the bytes of one lie behind those of the other.
+    bool overlaps(const Span& o) const {
+        if (end() <= o.at || o.end() <= at) return false;
+        auto apart = [](int64_t d, int64_t period, int64_t n, int64_t n_other) {
+            d = (d % period + period) % period;  // where the other's bytes start in this one's period
+            return d >= n && d + n_other <= period;
+        };
+        const int64_t d = (int64_t)(o.at - at);
+        if (B > 1 && o.B > 1 && stride_b == o.stride_b && apart(d, stride_b, each(), o.each())) return false;
+        const bool rows_in_step = stride_t == o.stride_t && (B == 1 || stride_b % stride_t == 0) &&
+                                  (o.B == 1 || o.stride_b % stride_t == 0);
+        return !(rows_in_step && apart(d, stride_t, row, o.row));
+    }
 };
 Span span_of(const void* p, int64_t B, int64_t stride_b, int64_t rows, int64_t stride_t, int64_t row) {
-    const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-    return {lo, lo + (uintptr_t)((B - 1) * stride_b + (rows - 1) * stride_t + row)};
+    return {reinterpret_cast<uintptr_t>(p), B, stride_b, rows, stride_t, row};
 }
 
 }  // namespace

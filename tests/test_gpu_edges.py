@@ -1,0 +1,40 @@
+"""Calls that the documentation allows at the edges: views of one array, calls from several threads, expired waits of the eviction,
+token counts that cannot be, the quantiser at every border."""
+import numpy as np
+import pytest
+import torch
+
+from mla_testutil import as_f64
+from oracle import cache_oracle as co
+from test_gpu_packed import TINY, V3, attend_case, decode_inputs, dims_of, i32, make_cache, rand
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("g", [V3, TINY], ids=["v3", "tiny"])
+def test_views_between_each_other(lib, g):
+    # earlier and later weights, the cache and where it is cut down to: halves of one array, and columns of one array
+    H, d_c, d_r, _, _, dt = g
+    dims, T, B, rows, width = dims_of(lib, g), (300, 129), 2, 300, d_c + d_r
+    cache, q = rand(1, B, rows, width, dtype=dt), rand(2, B, 1, H, width, dtype=dt, std=0.25)
+    lse, prev = rand(3, B, 1, H) + 5, rand(4, B, rows).abs()
+    want = lib.accumulate_weights(dims, q, lse, cache, i32(*T), torch.zeros(B, rows, device="cuda"), prev=prev)
+    both = torch.zeros(B, 2, rows, device="cuda")
+    both[:, 0] = prev
+    lib.accumulate_weights(dims, q, lse, cache, i32(*T), both[:, 1], prev=both[:, 0])
+    assert torch.equal(both[:, 1], want) and torch.equal(both[:, 0], prev)
+
+    budget = 100
+    out, ow, n = torch.zeros(B, budget, width, dtype=dt, device="cuda"), torch.zeros(B, budget, device="cuda"), i32(0, 0)
+    lib.evict(dims, cache, want, i32(*T), budget, 3, 20, out=out, out_weights=ow, out_seqlens=n)
+    half = torch.zeros(B, 2, rows, width, dtype=dt, device="cuda")
+    beside = torch.zeros(B, rows, 2, width, dtype=dt, device="cuda")
+    for one in (half, beside):
+        a, b = (one[:, 0], one[:, 1]) if one is half else (one[:, :, 0], one[:, :, 1])
+        a.copy_(cache)
+        both[:, 0], m = want, i32(0, 0)
+        both[:, 1] = 0
+        lib.evict(dims, a, both[:, 0], i32(*T), budget, 3, 20, out=b, out_weights=both[:, 1], out_seqlens=m)
+        assert torch.equal(a, cache) and torch.equal(b[:, :budget], out) and not b[:, budget:].any()
+        assert torch.equal(both[:, 0], want) and torch.equal(both[:, 1, :budget], ow) and torch.equal(m, n)
+    assert lib.device_status() == 0
