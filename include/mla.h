@@ -137,7 +137,8 @@ int mla_decode(const mla_dims_t* dims, const void* q_nope, const void* q_rope,
  *         device at once, for which mla_workspace_bytes() sizes the scratch).
  *   overhead_tiles: scheduling cost charged per query token (each of the
  *         B * q_len tokens is scheduled on its own), in 64-key tiles
- *         (negative = default, 2).
+ *         (negative = default, 2).  Refused where all sequences' tiles and
+ *         charges could pass 2^24.
  *   min_tiles: smallest piece of a token's keys one cluster takes, in 64-key tiles
  *         (0 = default, 2); larger values mean fewer split partials to merge.
  *         A batch whose sequences all have the same length is cut at sequence

@@ -129,6 +129,12 @@ int choose_path(const Problem& p, int q_len, const mla_decode_opts_t* o, bool* f
     return MLA_OK;
 }
 
+int check_split(const Problem& p, int T_max, const mla_decode_opts_t* o) {
+    if (o && o->overhead_tiles > 0 && p.B * (((int64_t)T_max + 63) / 64 + o->overhead_tiles) > kMaxUnits)
+        return fail(MLA_ERR_ARG, "opts->overhead_tiles %d is too large for %d sequences of up to %d rows", o->overhead_tiles, p.B, T_max);
+    return MLA_OK;
+}
+
 int pairs_for(const mla_decode_opts_t* o) {
     // At most the clusters that fit on the device at once: more would only
     // run in a second wave, and mla_workspace_bytes() sizes for that many.
@@ -267,7 +273,7 @@ int mla_attend_latent(const mla_dims_t* dims, const void* q_hat, const mla_cache
     p.q_len = q_len;
     bool fast;
     rc = choose_path(p, q_len, opts, &fast);
-    if (rc) return rc;
+    if (rc || (rc = check_split(p, cv.T_max, opts))) return rc;
     int* status = device_status_ptr();
     if (!status) return fail(MLA_ERR_CUDA, "no CUDA device / status word");
     cudaError_t e;
@@ -327,7 +333,7 @@ int mla_decode_ex(const mla_dims_t* dims, const void* q_nope, const void* q_rope
     p.q_len = q_len;
     bool fast;
     rc = choose_path(p, q_len, opts, &fast);
-    if (rc) return rc;
+    if (rc || (rc = check_split(p, cv.T_max, opts))) return rc;
     const int pairs = fast ? pairs_for(opts) : 1;
     const DecodeLayout L = decode_layout(p, fast, pairs);
     if (!workspace || workspace_bytes < L.total + kWsAlign || !aligned16(workspace))

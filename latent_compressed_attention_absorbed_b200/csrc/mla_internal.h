@@ -58,6 +58,11 @@ int check_cache(const Problem& p, const mla_cache_t* c, int B, CacheView* v);
 // Which path serves the call; also what mla_last_path() then says.
 int choose_path(const Problem& p, int q_len, const mla_decode_opts_t* o, bool* fast);
 int pairs_for(const mla_decode_opts_t* o);
+// The planners count the tiles of all sequences, and what the options charge
+// beside them, in 32 bits, as units g L of the groups g: kMaxUnits times the
+// groups (one for two SMs at most) fits.  No cache in memory has as many tiles.
+constexpr int kMaxUnits = 1 << 24;
+int check_split(const Problem& p, int T_max, const mla_decode_opts_t* o);
 constexpr size_t kWsAlign = 256;
 void* align_ws(void* ws, size_t* bytes);
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }

@@ -190,7 +190,7 @@ int mla_attend_packed(const mla_dims_t* dims, const void* q_hat, const mla_cache
     if (rc) return rc;
     bool fast;
     rc = choose_path(p, q_len, opts, &fast);
-    if (rc) return rc;
+    if (rc || (rc = check_split(p, cv.T_max, opts))) return rc;
     int* status = device_status_ptr();
     if (!status) return set_error(MLA_ERR_CUDA, "no CUDA device / status word");
     if (!fast)
@@ -222,7 +222,7 @@ int mla_decode_packed(const mla_dims_t* dims, const void* q_nope, const void* q_
         return set_error(MLA_ERR_ALIGN, "misaligned pointer");
     CacheView cv;
     rc = check_packed_cache(p, cache, B, &cv);
-    if (rc) return rc;
+    if (rc || (rc = check_split(p, cv.T_max, opts))) return rc;
     const size_t need = mla_packed_workspace_bytes(dims, B, q_len);
     if (!workspace || workspace_bytes < need || !aligned16(workspace))
         return set_error(MLA_ERR_WORKSPACE, "packed decode workspace needs %zu bytes (16-byte aligned), got %zu", need,
@@ -255,7 +255,7 @@ int mla_attend_latent_lse(const mla_dims_t* dims, const void* q_hat, const mla_c
     if (rc) return rc;
     bool fast;
     rc = choose_path(p, q_len, opts, &fast);
-    if (rc) return rc;
+    if (rc || (rc = check_split(p, cv.T_max, opts))) return rc;
     int* status = device_status_ptr();
     if (!status) return set_error(MLA_ERR_CUDA, "no CUDA device / status word");
     if (!fast)

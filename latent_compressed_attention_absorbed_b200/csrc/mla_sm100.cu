@@ -92,7 +92,7 @@ constexpr int kAbsorbStages = 2;
 // else the batch rounded up to 16 (the MMA still computes 128 rows; the rows
 // past the batch are never stored).
 int plan_ovh(int overhead_tiles) { return overhead_tiles < 0 ? 2 : overhead_tiles; }
-int plan_min_units(int min_tiles) { return min_tiles > 0 ? min_tiles : 2; }
+int plan_min_units(int min_tiles) { return min_tiles > 0 ? (min_tiles < kMaxUnits ? min_tiles : kMaxUnits) : 2; }
 int gemm_a_rows(int rows) { return rows >= 128 ? 128 : ((rows + 15) / 16) * 16; }
 constexpr int kProjStages = 4;
 constexpr int kProjNT = 64;
@@ -374,7 +374,7 @@ cudaError_t sm100_attend_packed(const Problem& p, const void* q_hat, const Cache
     a.q_len = p.q_len;
     a.T_max = cache.T_max;
     a.ovh = opts && opts->overhead_tiles >= 0 ? opts->overhead_tiles : 1;
-    a.min_units = opts && opts->min_tiles > 0 ? opts->min_tiles : 1;
+    a.min_units = opts && opts->min_tiles > 0 ? plan_min_units(opts->min_tiles) : 1;
     a.scale_log2 = p.scale * 1.4426950408889634f;
     a.q_hat = (const __nv_bfloat16*)q_hat;
     a.o_lat = (__nv_bfloat16*)o_lat;

@@ -88,3 +88,25 @@ def test_no_view_that_shares_a_byte_is_taken(L, a):
             assert not (shares and rc == WORKSPACE), (B, x, y)
             if stride_b % stride_t == 0 and off % 160 == 0 and rc == ARG and B == 1:
                 assert shares, (B, x, y)
+
+
+# ------------------------------------------------------------------ options that would not fit the planners' 32 bits
+
+def test_charges_past_the_planners_range_are_refused(L, a):
+    d, B, T = ctypes.byref(TINY), 2, 4
+    full, packed = bd.Cache(a, B, T, 4 * 40, 40), bd.Cache(a, B, T, 4 * 64, 64)
+    p, big = P(a), 1 << 24
+
+    def calls(**o):
+        opts = ctypes.byref(bd.Library.opts(path=2, **o))   # (the CUDA-core form, which runs anywhere else)
+        return [L.mla_decode_ex(d, p, p, p, p, ctypes.byref(full), p, B, 1, p, None, 0, opts, None),
+                L.mla_attend_latent(d, p, ctypes.byref(full), p, B, 1, p, None, 0, opts, None),
+                L.mla_attend_latent_lse(d, p, ctypes.byref(full), p, B, 1, p, p, None, 0, opts, None),
+                L.mla_attend_packed(d, p, ctypes.byref(packed), p, B, 1, p, None, None, 0, opts, None),
+                L.mla_decode_packed(d, p, p, p, p, ctypes.byref(packed), p, None, B, 1, p, None, None, None, 0, opts, None)]
+    for charge in (2 ** 31 - 1, 2 ** 30, big, big // 2):
+        assert calls(overhead_tiles=charge) == [ARG] * 5
+        assert b"overhead_tiles" in L.mla_last_error()
+    if not torch.cuda.is_available():        # (with a device the other three would run on these host addresses)
+        for o in (dict(overhead_tiles=big // 2 - 1), dict(overhead_tiles=-5), dict(min_tiles=2 ** 31 - 1)):
+            assert calls(**o) == [WORKSPACE, CUDA, CUDA, CUDA, WORKSPACE]

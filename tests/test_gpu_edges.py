@@ -6,7 +6,7 @@ import torch
 
 from mla_testutil import as_f64
 from oracle import cache_oracle as co
-from test_gpu_packed import TINY, V3, attend_case, decode_inputs, dims_of, i32, make_cache, rand
+from test_gpu_packed import TINY, V3, attend_case, check_attention, decode_inputs, dims_of, i32, make_cache, rand
 
 pytestmark = pytest.mark.gpu
 
@@ -37,4 +37,22 @@ def test_views_between_each_other(lib, g):
         lib.evict(dims, a, both[:, 0], i32(*T), budget, 3, 20, out=b, out_weights=both[:, 1], out_seqlens=m)
         assert torch.equal(a, cache) and torch.equal(b[:, :budget], out) and not b[:, budget:].any()
         assert torch.equal(both[:, 0], want) and torch.equal(both[:, 1, :budget], ow) and torch.equal(m, n)
+    assert lib.device_status() == 0
+
+
+def test_largest_options_of_the_split(lib):
+    # a share that no batch fills is one cluster's; a charge far above the tiles only moves the cuts
+    T, q_len = (900, 77, 333), 2
+    dims = dims_of(lib, V3)
+    full = rand(9, 3, 900, 576, dtype=torch.bfloat16)
+    _, cache, rows, q, one, _ = attend_case(lib, V3, T, q_len, lib.opts(num_pairs=q_len))
+    for tiles in (2 ** 31 - 1, 2 ** 25):
+        opts = lib.opts(min_tiles=tiles)
+        assert torch.equal(lib.attend_packed(dims, q, cache, i32(*T), opts=opts), one)
+        assert torch.equal(lib.attend_latent(dims, q, full, i32(*T), opts=opts),
+                           lib.attend_latent(dims, q, full, i32(*T), opts=lib.opts(num_pairs=q_len)))
+    lse = torch.zeros(3, q_len, 128, device="cuda")
+    for charge in (1000, 2 ** 22):
+        o = lib.attend_packed(dims, q, cache, i32(*T), lse=lse, opts=lib.opts(overhead_tiles=charge))
+        check_attention(o, lse, q, rows, T, q_len, V3, 192 ** -0.5, f"charge {charge}")
     assert lib.device_status() == 0
