@@ -387,12 +387,23 @@ int mla_accumulate_weights(const mla_dims_t* dims, const void* q_hat, const floa
  * appended to again, the caller sets its weight to zero.  A sequence with a
  * negative length or one above T_max keeps nothing and flags
  * MLA_STATUS_BAD_SEQLEN.  The workspace is of mla_evict_workspace_bytes()
- * bytes, 16-byte aligned, the call's until the stream reaches its end. */
+ * bytes, 16-byte aligned, the call's until the stream reaches its end.
+ * In place, the parts of a sequence wait for one another; a wait that runs
+ * out flags MLA_STATUS_TIMEOUT, and the cache, its weights and lengths are
+ * then undefined (parts have moved, and the lengths count the kept rows). */
 size_t mla_evict_workspace_bytes(const mla_dims_t* dims, int32_t cache_format, int32_t B, int32_t budget);
 int mla_evict(const mla_dims_t* dims, const mla_cache_t* cache, int32_t cache_format, const float* weights,
               int64_t weights_stride, const int32_t* seqlens, int32_t B, int32_t budget, int32_t n_sink,
               int32_t n_recent, const mla_cache_t* out_cache, float* out_weights, int64_t out_weights_stride,
               int32_t* out_seqlens, int32_t* kept, void* workspace, size_t workspace_bytes, mla_stream_t stream);
+
+/* mla_evict with options (NULL: defaults).  wait_limit_ns applies, and withhold_tile as a test hook: a value k > 0 keeps
+ * the k-th part of each sequence from being announced, so that the parts which wait for it in place run out. */
+int mla_evict_ex(const mla_dims_t* dims, const mla_cache_t* cache, int32_t cache_format, const float* weights,
+                 int64_t weights_stride, const int32_t* seqlens, int32_t B, int32_t budget, int32_t n_sink,
+                 int32_t n_recent, const mla_cache_t* out_cache, float* out_weights, int64_t out_weights_stride,
+                 int32_t* out_seqlens, int32_t* kept, void* workspace, size_t workspace_bytes,
+                 const mla_decode_opts_t* opts, mla_stream_t stream);
 
 /* ---------------------------------------------------------------- status */
 

@@ -33,7 +33,7 @@ EXPORTS = ["mla_append_cache", "mla_workspace_bytes", "mla_decode", "mla_decode_
            "mla_version", "mla_decode_no_alloc", "mla_append_from_hidden", "mla_append_from_hidden_workspace_bytes",
            "mla_output_projection", "mla_output_projection_workspace_bytes", "mla_packed_row_bytes", "mla_append_packed",
            "mla_append_rows", "mla_load_packed", "mla_packed_workspace_bytes", "mla_attend_packed", "mla_decode_packed",
-           "mla_attend_latent_lse", "mla_accumulate_weights", "mla_evict_workspace_bytes", "mla_evict"]
+           "mla_attend_latent_lse", "mla_accumulate_weights", "mla_evict_workspace_bytes", "mla_evict", "mla_evict_ex"]
 
 
 class Dims(ctypes.Structure):
@@ -96,6 +96,9 @@ _SIGS = {
     "mla_evict_workspace_bytes": ([ctypes.POINTER(Dims), _I, _I, _I], ctypes.c_size_t),
     "mla_evict": ([ctypes.POINTER(Dims), ctypes.POINTER(Cache), _I, _P, ctypes.c_int64, _P, _I, _I, _I, _I,
                    ctypes.POINTER(Cache), _P, ctypes.c_int64, _P, _P, _P, ctypes.c_size_t, _P], ctypes.c_int),
+    "mla_evict_ex": ([ctypes.POINTER(Dims), ctypes.POINTER(Cache), _I, _P, ctypes.c_int64, _P, _I, _I, _I, _I,
+                      ctypes.POINTER(Cache), _P, ctypes.c_int64, _P, _P, _P, ctypes.c_size_t, ctypes.POINTER(Opts), _P],
+                     ctypes.c_int),
     "mla_device_status": ([_P, ctypes.POINTER(_I)], ctypes.c_int),
     "mla_last_error": ([], ctypes.c_char_p),
     "mla_last_path": ([], ctypes.c_char_p),
@@ -519,7 +522,7 @@ class Library:
         return int(self.lib.mla_evict_workspace_bytes(ctypes.byref(dims), fmt, B, budget))
 
     def evict(self, dims: Dims, cache, weights, seqlens, budget: int, n_sink: int = 0, n_recent: int = 0, out=None,
-              out_weights=None, out_seqlens=None, kept=None, workspace=None, stream=None):
+              out_weights=None, out_seqlens=None, kept=None, workspace=None, opts: Optional[Opts] = None, stream=None):
         """Cuts sequences of more than ``budget`` rows down to the first n_sink, the last n_recent and the rows between
         with the largest weights, in their order.  In place unless ``out`` / ``out_weights`` / ``out_seqlens`` are
         given; ``kept`` (int32 [B, budget]) receives the kept rows' indexes, -1 past their number."""
@@ -545,9 +548,9 @@ class Library:
         _expect(kept, "kept", torch.int32, (B, budget), dev)
         ws = self._scratch(workspace, lambda: self.evict_workspace_bytes(dims, B, budget, fmt == CACHE_PACKED), dev,
                            stream)
-        self._call(self.lib.mla_evict, dev, stream, dims, cd, fmt, weights.data_ptr(), sw, seqlens.data_ptr(), B, budget,
+        self._call(self.lib.mla_evict_ex, dev, stream, dims, cd, fmt, weights.data_ptr(), sw, seqlens.data_ptr(), B, budget,
                    n_sink, n_recent, od, out_weights.data_ptr(), so, out_seqlens.data_ptr(),
-                   None if kept is None else kept.data_ptr(), ws.data_ptr(), ws.numel())
+                   None if kept is None else kept.data_ptr(), ws.data_ptr(), ws.numel(), opts)
 
     def device_status(self, stream=None) -> int:
         """Synchronises the stream, returns and clears the device status bits."""

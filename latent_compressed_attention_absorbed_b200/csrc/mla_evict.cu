@@ -352,13 +352,13 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(EvictArgs a, E
         __threadfence();
         __syncthreads();  // every thread's loads are done
         if (tid == 0) {
-            atomicExch(&loaded[chunk], 1);
+            if (chunk != a.withhold_chunk) atomicExch(&loaded[chunk], 1);
             const int c0 = s_wait[0] / s.chunk_rows, c1 = (s_wait[1] - 1) / s.chunk_rows;
             bool ok = true;
             for (int c = c0; c <= c1 && c < chunk && s_wait[1] > s_wait[0]; ++c) {
                 const uint64_t start = sm100::global_timer_ns();
                 while (atomicAdd(&loaded[c], 0) == 0) {
-                    if (sm100::global_timer_ns() - start > MLA_WAIT_LIMIT_NS) {
+                    if (sm100::global_timer_ns() - start > a.wait_limit_ns) {
                         ok = false;
                         break;
                     }
@@ -408,7 +408,9 @@ size_t evict_workspace(int B, int budget, int row_bytes) {
     return evict_layout(B, budget, row_bytes, &s, nullptr);
 }
 
-cudaError_t evict_launch(const EvictArgs& a, void* workspace, cudaStream_t st) {
+cudaError_t evict_launch(const EvictArgs& args, void* workspace, cudaStream_t st) {
+    EvictArgs a = args;
+    if (a.wait_limit_ns == 0) a.wait_limit_ns = MLA_WAIT_LIMIT_NS;
     EvictScratch s;
     evict_layout(a.B, a.budget, a.row_bytes, &s, workspace);
     const int64_t blocks = (int64_t)a.B * s.chunks;

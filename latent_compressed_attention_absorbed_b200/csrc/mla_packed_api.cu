@@ -327,6 +327,15 @@ int mla_evict(const mla_dims_t* dims, const mla_cache_t* cache, int32_t cache_fo
               int64_t weights_stride, const int32_t* seqlens, int32_t B, int32_t budget, int32_t n_sink,
               int32_t n_recent, const mla_cache_t* out_cache, float* out_weights, int64_t out_weights_stride,
               int32_t* out_seqlens, int32_t* kept, void* workspace, size_t workspace_bytes, mla_stream_t stream) {
+    return mla_evict_ex(dims, cache, cache_format, weights, weights_stride, seqlens, B, budget, n_sink, n_recent, out_cache,
+                        out_weights, out_weights_stride, out_seqlens, kept, workspace, workspace_bytes, nullptr, stream);
+}
+
+int mla_evict_ex(const mla_dims_t* dims, const mla_cache_t* cache, int32_t cache_format, const float* weights,
+                 int64_t weights_stride, const int32_t* seqlens, int32_t B, int32_t budget, int32_t n_sink,
+                 int32_t n_recent, const mla_cache_t* out_cache, float* out_weights, int64_t out_weights_stride,
+                 int32_t* out_seqlens, int32_t* kept, void* workspace, size_t workspace_bytes,
+                 const mla_decode_opts_t* opts, mla_stream_t stream) {
     set_error(MLA_OK, "%s", "");
     Problem p;
     int rc = check_dims(dims, &p);
@@ -384,6 +393,8 @@ int mla_evict(const mla_dims_t* dims, const mla_cache_t* cache, int32_t cache_fo
     if (seqlens != out_seqlens && span_of(seqlens, 1, 0, B, 4, 4).overlaps(span_of(out_seqlens, 1, 0, B, 4, 4)))
         return set_error(MLA_ERR_ARG, "out_seqlens overlaps seqlens: pass the same array, or one apart from it");
     a.in_place = rows_same || weights_same;
+    a.wait_limit_ns = opts && opts->wait_limit_ns > 0 ? (uint64_t)opts->wait_limit_ns : 0;
+    a.withhold_chunk = opts && opts->withhold_tile > 0 ? opts->withhold_tile - 1 : -1;
     const size_t need = evict_workspace(B, budget, a.row_bytes) + kWsAlign;
     if (!workspace || workspace_bytes < need || !aligned16(workspace))
         return set_error(MLA_ERR_WORKSPACE, "evict workspace needs %zu bytes (16-byte aligned), got %zu", need, workspace_bytes);

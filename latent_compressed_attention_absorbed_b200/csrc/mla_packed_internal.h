@@ -43,6 +43,8 @@ struct EvictArgs {
     int32_t* seqlens_out;
     int32_t* kept_out;  // [B][budget], or NULL
     bool in_place;      // rows or weights are moved within their own buffer
+    uint64_t wait_limit_ns;  // 0: the default
+    int withhold_chunk;  // test hook (>= 0): this chunk of a sequence does not say that it is loaded (see mla.h)
     int* status;
 };
 size_t evict_workspace(int B, int budget, int row_bytes);

@@ -56,3 +56,37 @@ def test_largest_options_of_the_split(lib):
         o = lib.attend_packed(dims, q, cache, i32(*T), lse=lse, opts=lib.opts(overhead_tiles=charge))
         check_attention(o, lse, q, rows, T, q_len, V3, 192 ** -0.5, f"charge {charge}")
     assert lib.device_status() == 0
+
+
+# ------------------------------------------------------------------ the eviction's waits
+
+@pytest.mark.parametrize("packed", [False, True])
+def test_evict_expired_wait(lib, packed):
+    # the second part of every sequence does not say that its rows are loaded: the third, which moves over them, gives up after
+    # 20 ms; the call reports it and ends, and the next one with the same workspace is right
+    dims, B, rows, budget = dims_of(lib, V3), 3, 5000, 4000
+    width = 416 if packed else 576
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    raw = torch.randint(0, 256, (B, rows, width * (1 if packed else 2)), generator=gen, device="cuda", dtype=torch.uint8)
+    cache = raw if packed else raw.view(torch.bfloat16)
+    weights, T = rand(2, B, rows).abs(), (5000, 4500, 4000)
+    bits = lambda t: t.view(torch.uint8)
+    work = torch.empty(lib.evict_workspace_bytes(dims, B, budget, packed), dtype=torch.uint8, device="cuda")
+
+    def run(**o):
+        c, w, n = cache.clone(), weights.clone(), i32(*T)
+        lib.evict(dims, c, w, n, budget, 4, 500, workspace=work, opts=lib.opts(**o) if o else None)
+        return c, w, n, lib.device_status()
+    c, w, n, status = run()
+    assert status == 0 and n.tolist() == [4000] * 3
+    *_, status = run(wait_limit_ns=20_000_000, withhold_tile=2)
+    assert status == 4
+    for o in ({}, dict(wait_limit_ns=20_000_000)):
+        c2, w2, n2, status = run(**o)
+        assert status == 0 and torch.equal(bits(c2), bits(c)) and torch.equal(w2, w) and torch.equal(n2, n)
+    # apart from the cache nothing waits
+    out, ow, on = torch.zeros_like(cache), torch.zeros_like(weights), i32(0, 0, 0)
+    lib.evict(dims, cache, weights, i32(*T), budget, 4, 500, out=out, out_weights=ow, out_seqlens=on, workspace=work,
+              opts=lib.opts(wait_limit_ns=1, withhold_tile=2))
+    assert lib.device_status() == 0 and torch.equal(on, n)
+    assert torch.equal(bits(out[:, :budget].contiguous()), bits(c[:, :budget].contiguous()))
