@@ -37,7 +37,7 @@ constexpr int kHeads = 128;  // H
 constexpr int kLinNT = 64;
 constexpr int kLinStages = 4;
 using LinC = LinCfg<kLinNT, kLinStages>;
-bool g_smem_linear[kMaxDev];
+DoneFlags g_smem_linear;
 constexpr int kAppendRow = kLat + kRope;  // 576 outputs per token
 constexpr float kRmsEps = 1e-6f;          // rms_norm_eps of the V3 configuration
 

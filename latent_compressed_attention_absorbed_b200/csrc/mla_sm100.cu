@@ -83,9 +83,9 @@ __global__ void append_v3_kernel(const __nv_bfloat16* __restrict__ c_kv, const _
     MLA_KT(kKtAppend, 2);
 }
 
-bool g_smem_absorb[kMaxDev], g_smem_project[kMaxDev], g_smem_attend[2][kMaxDev], g_smem_packed[kMaxDev];
-bool g_smem_weights[2][kMaxDev];
-bool g_smem_absorb_gemv[4][kMaxDev], g_smem_project_gemv[4][kMaxDev];
+DoneFlags g_smem_absorb, g_smem_project, g_smem_attend[2], g_smem_packed;
+DoneFlags g_smem_weights[2];
+DoneFlags g_smem_absorb_gemv[4], g_smem_project_gemv[4];
 
 constexpr int kAbsorbStages = 2;
 // Rows of the A tile a GEMM CTA loads: all 128 when the batch fills them,
@@ -415,7 +415,7 @@ cudaError_t sm100_attend_packed(const Problem& p, const void* q_hat, const Cache
 template <bool kPacked>
 static void weights_split(const Problem& p, int T_max, int* ranks, int* clusters) {
     using C = wt::Cfg<kPacked>;
-    static int most[4][kMaxDev];  // clusters of 2, 4 and 8 CTAs that run at once (0: not asked yet)
+    static std::atomic<int> most[4][kMaxDev];  // clusters of 2, 4 and 8 CTAs that run at once (0: not asked yet)
     const int sms = device_sm_count();
     *ranks = 1;
     *clusters = sms;
@@ -426,7 +426,7 @@ static void weights_split(const Problem& p, int T_max, int* ranks, int* clusters
     const int64_t alone = (units + sms - 1) / sms;
     double best = p.q_len * (double)(alone + pass * ((alone + wt::kBlock - 1) / wt::kBlock));
     for (int k = 1; k <= 3 && (1 << k) <= p.q_len; ++k) {
-        int& n = most[k][dev];
+        int n = most[k][dev].load(std::memory_order_relaxed);
         if (n == 0) {
             cudaLaunchConfig_t cfg;
             memset(&cfg, 0, sizeof(cfg));
@@ -445,6 +445,7 @@ static void weights_split(const Problem& p, int T_max, int* ranks, int* clusters
                 found = -1;
             }
             n = found;
+            most[k][dev].store(n, std::memory_order_relaxed);
         }
         if (n < 1) continue;
         const int64_t share = (units + n - 1) / n;

@@ -7,6 +7,7 @@
 #include <cuda_runtime.h>
 #include <string.h>
 
+#include <atomic>
 #include <utility>
 
 namespace mla {
@@ -17,14 +18,18 @@ typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t,
                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
+// (What is found out once and kept, here and below, is atomic: calls of several
+// threads may find it out at the same time.)
 inline EncodeTiledFn encode_fn() {
-    static EncodeTiledFn fn = nullptr;
+    static std::atomic<EncodeTiledFn> kept{nullptr};
+    EncodeTiledFn fn = kept.load(std::memory_order_relaxed);
     if (!fn) {
         void* p = nullptr;
         cudaDriverEntryPointQueryResult q;
         if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
             q == cudaDriverEntryPointSuccess)
             fn = reinterpret_cast<EncodeTiledFn>(p);
+        kept.store(fn, std::memory_order_relaxed);
     }
     return fn;
 }
@@ -75,14 +80,15 @@ inline bool make_map_2d(CUtensorMap* m, const void* base, uint64_t d0, uint64_t 
 // and call site (`done` is that site's own flag array), so that later calls,
 // including ones under stream capture, make no attribute calls.
 constexpr int kMaxDev = 64;
+using DoneFlags = std::atomic<bool>[kMaxDev];
 template <typename K>
-inline cudaError_t set_smem(K kernel, int bytes, bool (&done)[kMaxDev]) {
+inline cudaError_t set_smem(K kernel, int bytes, DoneFlags& done) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    if (dev >= 0 && dev < kMaxDev && done[dev]) return cudaSuccess;
+    if (dev >= 0 && dev < kMaxDev && done[dev].load(std::memory_order_acquire)) return cudaSuccess;
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e == cudaSuccess && dev >= 0 && dev < kMaxDev) done[dev] = true;
+    if (e == cudaSuccess && dev >= 0 && dev < kMaxDev) done[dev].store(true, std::memory_order_release);
     return e;
 }
 // Launch with programmatic dependent launch allowed: the kernel may start

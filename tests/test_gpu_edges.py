@@ -90,3 +90,47 @@ def test_evict_expired_wait(lib, packed):
               opts=lib.opts(wait_limit_ns=1, withhold_tile=2))
     assert lib.device_status() == 0 and torch.equal(on, n)
     assert torch.equal(bits(out[:, :budget].contiguous()), bits(c[:, :budget].contiguous()))
+
+
+# ------------------------------------------------------------------ several threads
+
+def test_first_calls_of_several_threads_at_once(lib, tmp_path):
+    # a library of its own (a copy of the file), so that what is found out at the first call is found out by all threads at once
+    import shutil
+    import threading
+    from latent_compressed_attention_absorbed_b200 import binding
+    T, q_len = (700, 333), 2
+    dims = dims_of(lib, V3)
+    packed, _ = make_cache(lib, dims, V3, T)
+    full, q = rand(9, 2, 700, 576, dtype=torch.bfloat16), rand(3, 2, q_len, 128, 576, dtype=torch.bfloat16, std=0.25)
+    lse, seq = rand(8, 2, q_len, 128) + 5, i32(*T)
+
+    def calls(one, stream):
+        zeros = lambda: torch.zeros(2, 700, device="cuda")
+        with torch.cuda.stream(stream):
+            w = [one.accumulate_weights(dims, q, lse, c, seq, zeros()) for c in (full, packed)]
+            z = torch.zeros_like(lse)
+            o = [one.attend_packed(dims, q, packed, seq), one.attend_latent_lse(dims, q, full, seq, z), z]
+            c, n = full.clone(), seq.clone()
+            one.evict(dims, c, w[0], n, 100, 4, 20)
+        return w + o + [c[0, :100], n]
+    ref = calls(lib, torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    for attempt in range(3):
+        copy = tmp_path / f"copy{attempt}.so"
+        shutil.copy(lib.path, copy)
+        fresh = binding.Library(str(copy))
+        gate, got, streams = threading.Barrier(8), [None] * 8, [torch.cuda.Stream() for _ in range(8)]
+
+        def work(i):
+            gate.wait()
+            got[i] = calls(fresh, streams[i])
+        threads = [threading.Thread(target=work, args=(i,)) for i in range(8)]
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+        torch.cuda.synchronize()
+        for one in got:
+            assert one is not None and all(torch.equal(a, b) for a, b in zip(one, ref))
+        assert fresh.device_status() == 0
