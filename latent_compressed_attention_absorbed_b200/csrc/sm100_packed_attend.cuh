@@ -683,7 +683,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_wait(bar(kRopeFull), (n_load - 1) & 1, lim);
         }
     }
-    if (warp == 1 && lane == 0) mma_commit(bar(kDrain));
+    if (warp == 1 && elect_one()) mma_commit(bar(kDrain));  // (a commit covers the products of the thread that makes it)
     if (warp == 1) mbar_wait(bar(kDrain), 0, lim);
     if (aborted && threadIdx.x == 0) atomicOr(args.status, MLA_STATUS_TIMEOUT);
     tc_fence_before();

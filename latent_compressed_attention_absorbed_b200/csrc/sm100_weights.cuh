@@ -456,7 +456,7 @@ __global__ void __launch_bounds__(Cfg<kPacked>::kThreads, 1)
         const int nst = warp == 0 ? (kPacked ? C::kRawStages : C::kRing) : (warp == 2 ? kQChunks : 1);
         for (int x = n_load > nst ? n_load - nst : 0; x < n_load; ++x) mbar_wait(bar(first + x % nst), (x / nst) & 1, lim);
     }
-    if (warp == 1 && lane == 0) mma_commit(bar(C::kDrain));
+    if (warp == 1 && elect_one()) mma_commit(bar(C::kDrain));  // (a commit covers the products of the thread that makes it)
     if (warp == 1) mbar_wait(bar(C::kDrain), 0, lim);
     if (aborted && threadIdx.x == 0) atomicOr(args.status, MLA_STATUS_TIMEOUT);
     tc_fence_before();
