@@ -334,7 +334,8 @@ int mla_attend_packed(const mla_dims_t* dims, const void* q_hat, const mla_cache
 /* mla_decode over a packed cache.  seqlens[b] counts the rows of the cache,
  * n_seen[b] the tokens the sequence has had (both including the q_len new
  * ones): query i sits at position n_seen[b] - q_len + i.  n_seen may be NULL
- * where no row has been evicted (then it is seqlens).  q_hat
+ * where no row has been evicted (then it is seqlens); one below q_len flags
+ * MLA_STATUS_BAD_SEQLEN, and that sequence's result has no meaning.  q_hat
  * [B][q_len][H][d_c + d_r] and lse [B][q_len][H] receive the folded queries
  * and the log-sum-exps, for mla_accumulate_weights; either may be NULL. */
 int mla_decode_packed(const mla_dims_t* dims, const void* q_nope, const void* q_rope, const void* W_UK,

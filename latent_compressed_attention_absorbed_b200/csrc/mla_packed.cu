@@ -276,7 +276,7 @@ constexpr int kMaxPerLane = 32;  // d_c <= 1024
 template <typename T, bool kPacked>
 __global__ void __launch_bounds__(kAttWarps * 32)
     attend_rows_kernel(Problem p, const T* __restrict__ q_hat, CacheView cache, const int32_t* __restrict__ seqlens,
-                       T* __restrict__ o_lat, float* __restrict__ lse, int* status) {
+                       const int32_t* __restrict__ n_seen, T* __restrict__ o_lat, float* __restrict__ lse, int* status) {
     extern __shared__ float smem[];
     const int row = p.d_c + p.d_r;
     float* sq = smem;            // [row]
@@ -289,6 +289,7 @@ __global__ void __launch_bounds__(kAttWarps * 32)
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int T_b = seqlens[b];
     T* out = o_lat + ((size_t)u * p.H + h) * p.d_c;
+    if (n_seen && i == 0 && h == 0 && threadIdx.x == 0 && n_seen[b] < p.q_len) atomicOr(status, MLA_STATUS_BAD_SEQLEN);
     if (T_b < p.q_len || T_b > cache.T_max) {
         if (threadIdx.x == 0) {
             atomicOr(status, MLA_STATUS_BAD_SEQLEN);
@@ -418,11 +419,11 @@ cudaError_t load_t(const Problem& p, const CacheView& cache, const int32_t* rows
 }
 
 template <typename T, bool kPacked>
-cudaError_t attend_rows_t(const Problem& p, const void* q_hat, const CacheView& cache, const int32_t* seqlens, void* o_lat,
-                          float* lse, int* status, cudaStream_t st) {
+cudaError_t attend_rows_t(const Problem& p, const void* q_hat, const CacheView& cache, const int32_t* seqlens,
+                          const int32_t* n_seen, void* o_lat, float* lse, int* status, cudaStream_t st) {
     const size_t smem = sizeof(float) * ((p.d_c + p.d_r) + 2 * kAttWarps + (size_t)kAttWarps * p.d_c);  // at most 38 KB
     attend_rows_kernel<T, kPacked><<<(unsigned)((size_t)p.B * p.q_len * p.H), kAttWarps * 32, smem, st>>>(
-        p, (const T*)q_hat, cache, seqlens, (T*)o_lat, lse, status);
+        p, (const T*)q_hat, cache, seqlens, n_seen, (T*)o_lat, lse, status);
     return cudaGetLastError();
 }
 
@@ -452,12 +453,12 @@ cudaError_t packed_load(const Problem& p, const CacheView& cache, const int32_t*
 }
 
 cudaError_t generic_attend_rows(const Problem& p, bool packed, const void* q_hat, const CacheView& cache,
-                                const int32_t* seqlens, void* o_lat, float* lse, int* status, cudaStream_t st) {
-    if (p.dtype == MLA_DTYPE_F32)
-        return packed ? attend_rows_t<float, true>(p, q_hat, cache, seqlens, o_lat, lse, status, st)
-                      : attend_rows_t<float, false>(p, q_hat, cache, seqlens, o_lat, lse, status, st);
-    return packed ? attend_rows_t<__nv_bfloat16, true>(p, q_hat, cache, seqlens, o_lat, lse, status, st)
-                  : attend_rows_t<__nv_bfloat16, false>(p, q_hat, cache, seqlens, o_lat, lse, status, st);
+                                const int32_t* seqlens, const int32_t* n_seen, void* o_lat, float* lse, int* status,
+                                cudaStream_t st) {
+#define MLA_ATTEND(T, P) attend_rows_t<T, P>(p, q_hat, cache, seqlens, n_seen, o_lat, lse, status, st)
+    if (p.dtype == MLA_DTYPE_F32) return packed ? MLA_ATTEND(float, true) : MLA_ATTEND(float, false);
+    return packed ? MLA_ATTEND(__nv_bfloat16, true) : MLA_ATTEND(__nv_bfloat16, false);
+#undef MLA_ATTEND
 }
 
 cudaError_t generic_weights(const Problem& p, bool packed, const void* q_hat, const float* lse, const CacheView& cache,

@@ -100,6 +100,40 @@ PackedDecodeLayout packed_decode_layout(const Problem& p) {
     return L;
 }
 
+// mla_attend_packed; n_seen (NULL: not checked) as mla_decode_packed has it.
+int attend_packed(const mla_dims_t* dims, const void* q_hat, const mla_cache_t* cache, const int32_t* seqlens,
+                  const int32_t* n_seen, int32_t B, int32_t q_len, void* o_lat, float* lse, void* workspace,
+                  size_t workspace_bytes, const mla_decode_opts_t* opts, mla_stream_t stream) {
+    Problem p;
+    int rc = check_query(dims, B, q_len, &p);
+    if (rc) return rc;
+    if ((rc = check_packed_dims(p))) return rc;
+    if (B == 0) return MLA_OK;
+    if (!q_hat || !seqlens || !o_lat) return set_error(MLA_ERR_ARG, "NULL tensor pointer");
+    if (!aligned16(q_hat) || !aligned16(o_lat) || !aligned4(seqlens) || !aligned4(lse))
+        return set_error(MLA_ERR_ALIGN, "misaligned pointer");
+    CacheView cv;
+    rc = check_packed_cache(p, cache, B, &cv);
+    if (rc) return rc;
+    bool fast;
+    rc = choose_path(p, q_len, opts, &fast);
+    if (rc || (rc = check_split(p, cv.T_max, opts))) return rc;
+    int* status = device_status_ptr();
+    if (!status) return set_error(MLA_ERR_CUDA, "no CUDA device / status word");
+    if (!fast)
+        return cuda_error(generic_attend_rows(p, true, q_hat, cv, seqlens, n_seen, o_lat, lse, status, (cudaStream_t)stream),
+                          "packed attend launch");
+    const int pairs = pairs_for(opts);
+    const size_t need = sm100_attend_workspace_bytes(p, pairs) + kWsAlign;
+    if (!workspace || workspace_bytes < need || !aligned16(workspace))
+        return set_error(MLA_ERR_WORKSPACE, "packed attend workspace needs %zu bytes (16-byte aligned), got %zu", need,
+                         workspace_bytes);
+    workspace = align_ws(workspace, &workspace_bytes);
+    return cuda_error(sm100_attend_packed(p, q_hat, cv, seqlens, n_seen, o_lat, lse, workspace, workspace_bytes, pairs, status,
+                                          opts, (cudaStream_t)stream),
+                      "packed attend launch");
+}
+
 // The bytes a view can touch: B sequences of `rows` rows of `row` bytes.
 struct Span {
     uintptr_t at;
@@ -177,34 +211,7 @@ size_t mla_packed_workspace_bytes(const mla_dims_t* dims, int32_t B, int32_t q_l
 int mla_attend_packed(const mla_dims_t* dims, const void* q_hat, const mla_cache_t* cache, const int32_t* seqlens,
                       int32_t B, int32_t q_len, void* o_lat, float* lse, void* workspace, size_t workspace_bytes,
                       const mla_decode_opts_t* opts, mla_stream_t stream) {
-    Problem p;
-    int rc = check_query(dims, B, q_len, &p);
-    if (rc) return rc;
-    if ((rc = check_packed_dims(p))) return rc;
-    if (B == 0) return MLA_OK;
-    if (!q_hat || !seqlens || !o_lat) return set_error(MLA_ERR_ARG, "NULL tensor pointer");
-    if (!aligned16(q_hat) || !aligned16(o_lat) || !aligned4(seqlens) || !aligned4(lse))
-        return set_error(MLA_ERR_ALIGN, "misaligned pointer");
-    CacheView cv;
-    rc = check_packed_cache(p, cache, B, &cv);
-    if (rc) return rc;
-    bool fast;
-    rc = choose_path(p, q_len, opts, &fast);
-    if (rc || (rc = check_split(p, cv.T_max, opts))) return rc;
-    int* status = device_status_ptr();
-    if (!status) return set_error(MLA_ERR_CUDA, "no CUDA device / status word");
-    if (!fast)
-        return cuda_error(generic_attend_rows(p, true, q_hat, cv, seqlens, o_lat, lse, status, (cudaStream_t)stream),
-                          "packed attend launch");
-    const int pairs = pairs_for(opts);
-    const size_t need = sm100_attend_workspace_bytes(p, pairs) + kWsAlign;
-    if (!workspace || workspace_bytes < need || !aligned16(workspace))
-        return set_error(MLA_ERR_WORKSPACE, "packed attend workspace needs %zu bytes (16-byte aligned), got %zu", need,
-                         workspace_bytes);
-    workspace = align_ws(workspace, &workspace_bytes);
-    return cuda_error(sm100_attend_packed(p, q_hat, cv, seqlens, o_lat, lse, workspace, workspace_bytes, pairs, status, opts,
-                                          (cudaStream_t)stream),
-                      "packed attend launch");
+    return attend_packed(dims, q_hat, cache, seqlens, nullptr, B, q_len, o_lat, lse, workspace, workspace_bytes, opts, stream);
 }
 
 int mla_decode_packed(const mla_dims_t* dims, const void* q_nope, const void* q_rope, const void* W_UK,
@@ -234,8 +241,8 @@ int mla_decode_packed(const mla_dims_t* dims, const void* q_nope, const void* q_
     void* o_lat = ws + L.o_lat;
     rc = mla_absorb_query(dims, q_nope, q_rope, W_UK, n_seen ? n_seen : seqlens, B, q_len, qh, opts, stream);
     if (rc) return rc;
-    rc = mla_attend_packed(dims, qh, cache, seqlens, B, q_len, o_lat, lse, ws + L.attend, L.total - L.attend, opts,
-                           stream);
+    rc = attend_packed(dims, qh, cache, seqlens, n_seen, B, q_len, o_lat, lse, ws + L.attend, L.total - L.attend, opts,
+                       stream);
     if (rc) return rc;
     return mla_project_out(dims, o_lat, W_UV, B * q_len, out, opts, stream);
 }
@@ -259,7 +266,7 @@ int mla_attend_latent_lse(const mla_dims_t* dims, const void* q_hat, const mla_c
     int* status = device_status_ptr();
     if (!status) return set_error(MLA_ERR_CUDA, "no CUDA device / status word");
     if (!fast)
-        return cuda_error(generic_attend_rows(p, false, q_hat, cv, seqlens, o_lat, lse, status, (cudaStream_t)stream),
+        return cuda_error(generic_attend_rows(p, false, q_hat, cv, seqlens, nullptr, o_lat, lse, status, (cudaStream_t)stream),
                           "attend launch");
     const int pairs = pairs_for(opts);
     const size_t need = sm100_attend_workspace_bytes(p, pairs) + kWsAlign;

@@ -13,16 +13,18 @@ cudaError_t rows_append(const Problem& p, bool packed, const void* c_kv, const v
                         const int32_t* rows, int n_tok, const CacheView& cache, int* status, cudaStream_t st);
 cudaError_t packed_load(const Problem& p, const CacheView& cache, const int32_t* rows, int n_tok, void* out, int* status,
                         cudaStream_t st);
-// CUDA-core forms, any geometry; lse may be NULL.
+// CUDA-core forms, any geometry; lse may be NULL.  n_seen (NULL: not checked):
+// token counts of the queries' positions, flagged where they are too small.
 cudaError_t generic_attend_rows(const Problem& p, bool packed, const void* q_hat, const CacheView& cache,
-                                const int32_t* seqlens, void* o_lat, float* lse, int* status, cudaStream_t st);
+                                const int32_t* seqlens, const int32_t* n_seen, void* o_lat, float* lse, int* status,
+                                cudaStream_t st);
 cudaError_t generic_weights(const Problem& p, bool packed, const void* q_hat, const float* lse, const CacheView& cache,
                             const int32_t* seqlens, float decay, const float* prev, float* weights, int64_t stride_w,
                             int* status, cudaStream_t st);
 
 // Tensor-core form (sm100_supported); the workspace is sm100_attend_workspace_bytes().
 cudaError_t sm100_attend_packed(const Problem& p, const void* q_hat, const CacheView& cache, const int32_t* seqlens,
-                                void* o_lat, float* lse, void* workspace, size_t ws_bytes, int num_pairs, int* status,
+                                const int32_t* n_seen, void* o_lat, float* lse, void* workspace, size_t ws_bytes, int num_pairs, int* status,
                                 const mla_decode_opts_t* opts, cudaStream_t st);
 
 cudaError_t sm100_weights(const Problem& p, bool packed, const void* q_hat, const float* lse, const CacheView& cache,

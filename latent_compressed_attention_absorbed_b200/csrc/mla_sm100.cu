@@ -350,7 +350,7 @@ cudaError_t sm100_attend(const Problem& p, const void* q_hat, const CacheView& c
 }
 
 cudaError_t sm100_attend_packed(const Problem& p, const void* q_hat, const CacheView& cache, const int32_t* seqlens,
-                                void* o_lat, float* lse, void* workspace, size_t ws_bytes, int num_pairs, int* status,
+                                const int32_t* n_seen, void* o_lat, float* lse, void* workspace, size_t ws_bytes, int num_pairs, int* status,
                                 const mla_decode_opts_t* opts, cudaStream_t st) {
     const int clusters = attend_clusters(num_pairs, p.q_len);
     if (clusters / p.q_len > kPlanMaxGroups) return cudaErrorInvalidValue;
@@ -370,6 +370,7 @@ cudaError_t sm100_attend_packed(const Problem& p, const void* q_hat, const Cache
     if (e != cudaSuccess) return e;
     pk::Args a;
     a.seqlens = seqlens;
+    a.n_seen = n_seen;
     a.B = p.B;
     a.q_len = p.q_len;
     a.T_max = cache.T_max;

@@ -127,6 +127,7 @@ static_assert(8 * (kBars + 2) <= 512, "barrier block too small");
 
 struct Args {
     const int32_t* seqlens;
+    const int32_t* n_seen;  // or NULL; only checked here
     int B, q_len, T_max;
     int ovh, min_units;  // of the split, in tiles
     float scale_log2;
@@ -214,6 +215,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool active = grp < groups;
     // Sequences with an invalid length: zeros, and -infinity for the log-sum-exps.
     for (int b = blockIdx.x; b < args.B; b += gridDim.x) {
+        if (args.n_seen && threadIdx.x == 0 && args.n_seen[b] < q_len) atomicOr(args.status, MLA_STATUS_BAD_SEQLEN);
         if (batch.valid(batch.len(b))) continue;
         if (threadIdx.x == 0) {
             atomicOr(args.status, MLA_STATUS_BAD_SEQLEN);

@@ -134,3 +134,20 @@ def test_first_calls_of_several_threads_at_once(lib, tmp_path):
         for one in got:
             assert one is not None and all(torch.equal(a, b) for a, b in zip(one, ref))
         assert fresh.device_status() == 0
+
+
+# ------------------------------------------------------------------ token counts
+
+@pytest.mark.parametrize("path", [0, 2])
+def test_token_counts_below_the_queries_are_flagged(lib, path):
+    T, q_len = (300, 40, 64), 2
+    dims, opts = dims_of(lib, V3), lib.opts(path=path)
+    cache, _ = make_cache(lib, dims, V3, T)
+    ins = decode_inputs(V3, 3, q_len)
+    seen = (300, 1000, 2)                    # (the smallest that can be)
+    ref = lib.decode_packed(dims, *ins, cache, i32(*T), n_seen=i32(*seen), opts=opts)
+    assert lib.device_status() == 0
+    for bad in (1, 0, -5, -2 ** 31):
+        out = lib.decode_packed(dims, *ins, cache, i32(*T), n_seen=i32(300, bad, 2), opts=opts)
+        assert lib.device_status() == 2
+        assert torch.equal(out[0], ref[0]) and torch.equal(out[2], ref[2])
