@@ -151,3 +151,35 @@ def test_token_counts_below_the_queries_are_flagged(lib, path):
         out = lib.decode_packed(dims, *ins, cache, i32(*T), n_seen=i32(300, bad, 2), opts=opts)
         assert lib.device_status() == 2
         assert torch.equal(out[0], ref[0]) and torch.equal(out[2], ref[2])
+
+
+# ------------------------------------------------------------------ the bf16 quantiser at every border
+
+def test_quantisation_of_every_bf16_latent_at_every_scale(lib):
+    # bf16 latents are quantised by arithmetic of their own.  For each of the 256 scales s: every bf16 value from s / 5 to 7 s, of both
+    # signs (all halves of a step that there are, and the numbers on both sides), in groups whose largest is 7 s
+    dims = dims_of(lib, (1, 512, 2, 4, 4, torch.bfloat16))
+    every = (np.arange(0x4653, dtype=np.uint32) << 16).view(np.float32)     # 0 .. 13440
+    groups = []
+    for s in co.SCALES:
+        v = every[(every >= s / 5) & (every <= 7 * s)]
+        v = np.r_[0.0, every[1], v, -v, -every[1]]
+        v = np.r_[v, np.zeros(-len(v) % 15)].reshape(-1, 15)
+        groups.append(np.c_[np.full(len(v), 7 * s), v])
+    x = np.concatenate(groups)
+    # and every bf16 magnitude as the largest of its group, with values below it
+    x = np.concatenate([x, every[:, None] * np.r_[1.0, -0.5, np.zeros(14)]])
+    x = np.r_[x, np.zeros((-len(x) % 32, 16))].reshape(1, -1, 512)
+    c = torch.from_numpy(x).to(torch.bfloat16).cuda()
+    n = c.shape[1]
+    cache = torch.zeros(1, n, lib.packed_row_bytes(dims), dtype=torch.uint8, device="cuda")
+    lib.append_packed(dims, cache, c, torch.zeros(1, n, 2, dtype=torch.bfloat16, device="cuda"), i32(0))
+    assert lib.device_status() == 0
+    q, code = co.quantise(as_f64(c)[0])
+    raw = cache[0].cpu().numpy()
+    np.testing.assert_array_equal(raw[:, 256:288], code)
+    np.testing.assert_array_equal(co.unpack_latents(raw, 512), co.quantised(as_f64(c)[0]))
+    np.testing.assert_array_equal(as_f64(lib.load_packed(dims, cache, i32(0), n))[0, :, :512], co.quantised(as_f64(c)[0]))
+    word = raw[:, :256].copy().view(np.uint32)
+    for e in range(8):                       # codes, too: 0 has one code at any scale
+        np.testing.assert_array_equal((word >> (4 * (e // 2) + 16 * (e % 2)) & 15).astype(int) - 8, q[:, e::8])
