@@ -412,7 +412,9 @@ cudaError_t sm100_attend_packed(const Problem& p, const void* q_hat, const Cache
 // the eight tiles whose sums it holds, by the cache's size, as the lengths lie on
 // the device.  One CTA against a cluster, in us: 1 x 600 packed rows with 16
 // queries 55 and 13, 1 x 4096 with 2 11.2 and 9.3, with 16 56 and 23; but 16 x
-// 2000 with 2 15.6 and 18.0, which the rule leaves to one.
+// 2000 with 2 15.6 and 18.0, which the rule leaves to one.  In a cache much longer
+// than its sequences the rule sees no clusters (1 x 600 rows with 16 queries: 13 us
+// by T_max 600, 56 to 64 by 131072), so callers who know a bound pass it as T_max.
 template <bool kPacked>
 static void weights_split(const Problem& p, int T_max, int* ranks, int* clusters) {
     using C = wt::Cfg<kPacked>;

@@ -453,6 +453,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 // p = 2^(s - m_used + 7)
                 const float mb = m_used == -CUDART_INF_F ? 0.f : kPShift - m_used;
+                // (A half meets a slot in every other of its phases, and a barrier's parity
+                // tells only neighbouring phases apart.  The phase between was waited for
+                // by the other half of the pair, one or two tiles ago, before the meeting
+                // at the named barrier above.)
                 if (ok && unit >= kSlots) ok = wait_peer(kSlotFree + slot, unit / kSlots + 1);
                 if (ok) {
                     const uint32_t stg = base + kOffStage + slot * kSlotBytes;
@@ -617,7 +621,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // (the vote has both values, so that neither load is under way when the slot is given back; a sum is never negative)
                 const bool scaled = __any_sync(0xffffffffu, f != 1.0f || l_part < 0.f);
                 if (u > u0 && scaled) {
-                    // O must hold everything before this unit when it is rescaled
+                    // O must hold everything before this unit when it is rescaled.  (The
+                    // phases of this barrier that were not waited for are complete: P of
+                    // unit u lands once the products of unit u - kSlots have returned its
+                    // slot, and commits complete in order, so unit u - 1 - kSlots is done.)
                     if (!wait(kPDone + (u - 1) % kSlots, (u - 1) / kSlots)) { ok = false; break; }
                     tc_fence_after();
 #pragma unroll 1

@@ -183,3 +183,30 @@ def test_quantisation_of_every_bf16_latent_at_every_scale(lib):
     word = raw[:, :256].copy().view(np.uint32)
     for e in range(8):                       # codes, too: 0 has one code at any scale
         np.testing.assert_array_equal((word >> (4 * (e // 2) + 16 * (e % 2)) & 15).astype(int) - 8, q[:, e::8])
+
+
+# ------------------------------------------------------------------ a bound on the lengths as T_max
+
+@pytest.mark.parametrize("packed", [False, True])
+def test_a_view_of_the_first_rows(lib, packed):
+    # the calls choose their split by T_max: a long cache seen through a view gives the bits of a cache of that length
+    T, q_len, bound, cap = (600, 77), 16, 640, 20000
+    dims = dims_of(lib, V3)
+    width, dt = (416, torch.uint8) if packed else (576, torch.bfloat16)
+    long = torch.full((2, cap, width), 0xFF if packed else float("nan"), dtype=dt, device="cuda")
+    long[:, :bound] = make_cache(lib, dims, V3, T, T_max=bound)[0] if packed else rand(9, 2, bound, 576, dtype=dt)
+    tight, view = long[:, :bound].contiguous(), long[:, :bound]
+    q, lse = rand(3, 2, q_len, 128, 576, dtype=torch.bfloat16, std=0.25), rand(8, 2, q_len, 128) + 5
+    want = lib.accumulate_weights(dims, q, lse, tight, i32(*T), torch.zeros(2, bound, device="cuda"))
+    w = torch.full((2, cap), -1.0, device="cuda")
+    lib.accumulate_weights(dims, q, lse, view, i32(*T), w)
+    assert all(torch.equal(w[b, :t], want[b, :t]) and torch.all(w[b, t:] == -1) for b, t in enumerate(T))
+    n, m = i32(*T), i32(*T)
+    lib.evict(dims, tight, want, n, 200, 4, 50)
+    behind = long[:, bound:].view(torch.uint8).clone()
+    lib.evict(dims, view, w, m, 200, 4, 50)
+    assert torch.equal(n, m) and torch.equal(tight.view(torch.uint8), view.contiguous().view(torch.uint8))
+    assert all(torch.equal(w[b, :t], want[b, :t]) for b, t in enumerate(T)) and torch.equal(long[:, bound:].view(torch.uint8), behind)
+    assert lib.device_status() == 0
+    lib.evict(dims, view, w, i32(bound + 1, 100), 200)   # a length past the bound
+    assert lib.device_status() == 2
