@@ -31,8 +31,8 @@
 //
 // Measured (B200, 128 heads; bursts of twenty calls, and in brackets calls in a
 // row for seconds): 1 x 4096 rows 28 us, most of it the latency of one tile and
-// of the merge; 64 x 4096 rows 104 us; 8 x 131072 rows 307 (348) us, 950 (840)
-// TFLOP/s; 128 x 2048..16384 rows with two queries 684 (780) us, 990 (870).  What holds the
+// of the merge; 64 x 4096 rows 104 us; 8 x 131072 rows 311 (350) us, 940 (830)
+// TFLOP/s; 128 x 2048..16384 rows with two queries 688 (776) us, 980 (870).  What holds the
 // long ones up is power: at 993 W the clock falls to 1.75 GHz, and fewer
 // instructions a value gained 5 % where deeper rings, other bank layouts and
 // earlier hand-offs, which only hide latency, gained nothing.  Code counts too:

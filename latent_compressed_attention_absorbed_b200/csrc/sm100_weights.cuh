@@ -26,11 +26,11 @@
 // eight tiles, each CTA takes some of the queries, and at the end the CTAs' sums
 // are added up through distributed shared memory, in the order of their ranks.
 //
-// Measured (B200, bursts): 1 x 4096 full-width rows 11 us (two thirds of it the
-// launch, Q-hat's load and the end); 8 x 65536..131072 rows 187 us, 5.1 TB/s, 0.79
-// of the copy's bandwidth (the power limit is reached there, with the clock at
-// 1.24 GHz); 64 x 2048..16384 packed rows with two queries 153 us, 0.69 of the
-// products' rate (181 us in a loop, at the power limit).
+// Measured (B200, bursts of twenty calls, and in brackets calls in a row for
+// seconds, at the power limit): 1 x 4096 full-width rows 11 us (two thirds of it
+// the launch, Q-hat's load and the end); 8 x 65536..131072 rows 169 (189) us, 5.8
+// (5.1) TB/s, 0.88 (0.79) of the copy's bandwidth; 64 x 2048..16384 packed rows
+// with two queries 156 (184) us, 0.67 (0.57) of the products' rate.
 //
 // Every wait is bounded; no warp waits on a barrier without a limit before
 // the common end, so a wait that expires ends the kernel in order.
